@@ -416,6 +416,96 @@ AXON_API axon_status axon_ssd_scan_fwd(
     void *y, float *h_out, int segments, void *workspace, size_t workspace_bytes, axon_stream_t stream);
 
 /*
+ * The gated delta rule: the SSD core's recurrence (one scalar decay per head)
+ * with an erase term, so a write replaces what the state held for its key.
+ * Per batch row b and value head h, with key head g = h / (H / G) and state
+ * S (P x N):
+ *   dt = softplus(dt_raw[b,t,h] + dt_bias[h]),  a = exp(-exp(A_log[h]) dt),
+ *   beta = sigmoid(b_raw[b,t,h]),
+ *   k^ = k[b,t,g,:] / sqrt(|k|^2 + 1e-6), q^ likewise  (qk_norm != 0; else k, q),
+ *   S  = a S (I - beta k^ k^^T) + beta v[b,t,h,:] k^^T,
+ *   y[b,t,h,:] = scale S q^.
+ * (dt is not clipped here: the erase term bounds the state, and a long memory
+ * wants decays of exactly 1.  With qk_norm == 0 keys longer than
+ * sqrt(2 / beta) let the state grow without bound.)
+ *
+ * axon_delta_scan_fwd, prefill.  Layouts: q, k (B,L,G,N) and v (B,L,H,P) io,
+ * consecutive tokens ldq, ldk, ldv elements apart (ldq, ldk >= G*N, ldv >=
+ * H*P, batch rows L of those apart), so slices of one projected row need no
+ * copy; dt_raw, b_raw (B,L,H) io; dt_bias, A_log (H) float32; y (B,L,H,P) io
+ * dense; h0 (B,H,P,N) float32 or NULL (zeros); h_out (B,H,P,N) float32, may
+ * be h0 itself.  N and P are 64 or 128, G divides H (else
+ * AXON_ERR_UNSUPPORTED).  lengths: NULL, or B device ints: row b has
+ * lengths[b] tokens (taken into 0 .. L); what lies behind is not used, y is
+ * not written there, and h_out is the state after the row's last token (h0
+ * for a row of no tokens).
+ *
+ * axon_delta_step, cached decode: one token for B sequences, L absent (q, k
+ * (B,G,N), v (B,H,P), rows ldq, ldk, ldv apart; dt_raw, b_raw (B,H); y
+ * (B,H,P)), state (B,H,P,N) float32 updated in place.
+ *
+ * `workspace` (16-byte aligned; may be NULL when the size is 0) holds
+ * axon_delta_workspace_bytes(B, L, H, G, P, N, io) bytes.  Every call writes
+ * what it reads there, so calls that may run at the same time (streams,
+ * captured graphs) need one each.  Pointers 16-byte aligned and ldq, ldk, ldv
+ * multiples of 8 (bf16) or 4 (f32), else AXON_ERR_ALIGNMENT; y, h_out and the
+ * workspace overlap no input (but h_out may be h0) nor each other
+ * (AXON_ERR_INVALID_ARG).  B, H <= 65535 and B*L*H <= 2^31, else
+ * AXON_ERR_UNSUPPORTED.  B == 0 or H == 0 is a no-op; L == 0 copies h0 (or
+ * zeros) to h_out.  Everything is float32 inside.  Other conventions as
+ * above.
+ */
+AXON_API size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io);
+
+AXON_API axon_status axon_delta_scan_fwd(
+    int B, int L, int H, int G, int P, int N, axon_dtype io,
+    const void *q, int ldq, const void *k, int ldk, const void *v, int ldv,
+    const void *dt_raw, const void *b_raw, const float *dt_bias, const float *A_log,
+    const int *lengths, const float *h0, float scale, int qk_norm,
+    void *y, float *h_out, void *workspace, size_t workspace_bytes, axon_stream_t stream);
+
+AXON_API axon_status axon_delta_step(
+    int B, int H, int G, int P, int N, axon_dtype io,
+    const void *q, int ldq, const void *k, int ldk, const void *v, int ldv,
+    const void *dt_raw, const void *b_raw, const float *dt_bias, const float *A_log,
+    float scale, int qk_norm, float *state, void *y, axon_stream_t stream);
+
+/*
+ * Grouped norm with a gate or activation, channels last: what follows a
+ * recurrent core before the output projection (a norm per head, D = P; or
+ * over wider groups).  x, z, y: `rows` rows of C channels, consecutive rows
+ * ldx, ldz, ldy elements apart; statistics per row and group of D channels
+ * (torch's group norm of a (rows, C) tensor, C / D groups).
+ *   t = x, or x f(z) with AXON_GATE_BEFORE
+ *   AXON_NORM_RMS:    n = t / sqrt(mean(t^2) + eps)
+ *   AXON_NORM_GROUP:  n = (t - m) / sqrt(mean((t - m)^2) + eps), m = mean(t)
+ *   o = n weight + bias
+ *   AXON_GATE_AFTER:  y = o f(z);  AXON_GATE_NONE: y = f(o) (z is ignored);
+ *   AXON_GATE_BEFORE: y = o
+ * with f(u) = u / (1 + exp(-u)) (SiLU) when act != 0, else f(u) = u.
+ * weight, bias: float32 or NULL (1 and 0), C values with per_channel != 0,
+ * else D values shared by the groups.  y may be x or z itself (same row
+ * stride), and otherwise overlaps no input (AXON_ERR_INVALID_ARG).  D divides
+ * C (AXON_ERR_INVALID_ARG) and is a multiple of 8 (bf16) or 4 (f32), as are
+ * ldx, ldz, ldy (AXON_ERR_ALIGNMENT); D <= 8192 and rows * C / D < 2^31, else
+ * AXON_ERR_UNSUPPORTED.  eps >= 0; a group of zeros with eps == 0 gives NaN.
+ * rows == 0 is a no-op.  Float32 inside, rounded once.
+ */
+typedef enum {
+    AXON_NORM_RMS = 0,
+    AXON_NORM_GROUP = 1
+} axon_norm_kind;
+typedef enum {
+    AXON_GATE_NONE = 0,
+    AXON_GATE_AFTER = 1,
+    AXON_GATE_BEFORE = 2
+} axon_norm_gate;
+AXON_API axon_status axon_gated_norm_fwd(
+    int rows, int C, int D, axon_dtype io, axon_norm_kind kind, axon_norm_gate gate, int act,
+    const void *x, int ldx, const void *z, int ldz, const float *weight, const float *bias, int per_channel,
+    float eps, void *y, int ldy, axon_stream_t stream);
+
+/*
  * The whole Axon-SSM layer around the layer core (Axon-SSM page, sections
  * "Gating" and "Selective mechanism"), bf16 io only:
  *

@@ -84,6 +84,10 @@ def _load(openmp: bool = False):
             lib.oracle_conv_silu.argtypes = [ctypes.c_int] * 4 + [_dp] * 5
             lib.oracle_ssd_scan.restype = ctypes.c_int
             lib.oracle_ssd_scan.argtypes = [ctypes.c_int] * 5 + [_dp] * 10
+            lib.oracle_delta_scan.restype = ctypes.c_int
+            lib.oracle_delta_scan.argtypes = [ctypes.c_int] * 6 + [_dp] * 9 + [ctypes.c_double, ctypes.c_int] + [_dp] * 2
+            lib.oracle_gated_norm.restype = ctypes.c_int
+            lib.oracle_gated_norm.argtypes = [ctypes.c_int] * 6 + [_dp] * 4 + [ctypes.c_double, _dp]
             lib.oracle_threads.restype = ctypes.c_int
             lib.oracle_threads.argtypes = []
             _libs[openmp] = lib
@@ -265,6 +269,43 @@ def ssd_scan(x, dt_raw, dt_bias, A_log, Bm, Cm, D, h0=None):
     if rc != 0:
         raise RuntimeError("oracle_ssd_scan failed")
     return y, h_out
+
+
+def delta_scan(q, k, v, dt_raw, b_raw, dt_bias, A_log, h0=None, lengths=None, scale=None, norm=True):
+    """The gated delta rule token by token, fp64.  q, k (B,L,G,N); v (B,L,H,P);
+    dt_raw, b_raw (B,L,H); dt_bias, A_log (H,); h0 (B,H,P,N) or None; lengths
+    (B,) or None.  Returns (y, h_out); y behind a row's end is 0."""
+    q, k, v, dt_raw, b_raw, dt_bias, A_log = (_f64(t) for t in (q, k, v, dt_raw, b_raw, dt_bias, A_log))
+    Bsz, L, H, P = v.shape
+    G, N = k.shape[2:]
+    hh = None if h0 is None else _f64(h0)
+    ln = None if lengths is None else _f64(lengths)
+    y = np.zeros((Bsz, L, H, P))
+    h_out = np.zeros((Bsz, H, P, N))
+    rc = _load().oracle_delta_scan(Bsz, L, H, G, P, N, _ptr(q), _ptr(k), _ptr(v), _ptr(dt_raw), _ptr(b_raw),
+                                   _ptr(dt_bias), _ptr(A_log), _ptr(ln), _ptr(hh),
+                                   float(N ** -0.5 if scale is None else scale), int(bool(norm)), _ptr(y), _ptr(h_out))
+    if rc != 0:
+        raise RuntimeError("oracle_delta_scan failed")
+    return y, h_out
+
+
+def gated_norm(x, D, kind="rms", gate=None, act=True, z=None, weight=None, bias=None, eps=1e-6):
+    """Grouped norm of the rows of x (..., C), groups of D channels, with a
+    gate ("after", "before") by z or an activation, fp64.  weight and bias hold
+    D or C values."""
+    x = _f64(x)
+    C = x.shape[-1]
+    z = None if z is None else _f64(z)
+    weight, bias = (None if t is None else np.ascontiguousarray(np.broadcast_to(_f64(t).reshape(-1, D), (C // D, D)))
+                    for t in (weight, bias))
+    y = np.zeros(x.shape)
+    rc = _load().oracle_gated_norm(x.size // max(C, 1), C, D, {"rms": 0, "group": 1}[kind],
+                                   {None: 0, "after": 1, "before": 2}[gate], int(bool(act)), _ptr(x), _ptr(z),
+                                   _ptr(weight), _ptr(bias), float(eps), _ptr(y))
+    if rc != 0:
+        raise RuntimeError("oracle_gated_norm failed")
+    return y
 
 
 def scan_channels(inputs: dict, channels, zoh=False):

@@ -274,3 +274,82 @@ int oracle_ssd_scan(int B, int L, int H, int P, int N, const double *x, const do
     free(S);
     return 0;
 }
+
+/*
+ * The gated delta rule (scalar decay and an erase term per value head): per
+ * batch row b, value head h, key head g = h / (H / G), state S (P x N)
+ *   dt = log(1 + exp(dt_raw + dt_bias)),  a = exp(-exp(A_log) dt),
+ *   beta = 1 / (1 + exp(-b_raw)),
+ *   k^ = k / sqrt(|k|^2 + 1e-6), q^ likewise (norm != 0; else as they are),
+ *   S[p][n] = a S[p][n] + beta (v[p] - a sum_m S[p][m] k^[m]) k^[n],
+ *   y[p] = scale sum_n S[p][n] q^[n].
+ * Layouts: q, k (B,L,G,N); v, y (B,L,H,P); dt_raw, b_raw (B,L,H); dt_bias,
+ * A_log (H); h0, h_out (B,H,P,N), h0 may be NULL.  lengths (B) or NULL: tokens
+ * behind a row's end are skipped and their y left as it was.
+ */
+int oracle_delta_scan(int B, int L, int H, int G, int P, int N, const double *q, const double *k, const double *v,
+                      const double *dt_raw, const double *b_raw, const double *dt_bias, const double *A_log,
+                      const double *lengths, const double *h0, double scale, int norm, double *y, double *h_out)
+{
+    if (B < 0 || L < 0 || H < 0 || G <= 0 || H % G || P <= 0 || N <= 0) return -1;
+    for (int b = 0; b < B; ++b)
+        for (int h = 0; h < H; ++h) {
+            double *S = h_out + ((size_t)b * H + h) * P * N;
+            for (int i = 0; i < P * N; ++i) S[i] = h0 ? h0[((size_t)b * H + h) * P * N + i] : 0.0;
+            const int g = h / (H / G);
+            int len = lengths ? (int)lengths[b] : L;
+            if (len > L) len = L;
+            for (int t = 0; t < len; ++t) {
+                const size_t tok = (size_t)b * L + t;
+                const double *kt = k + (tok * G + g) * N, *qt = q + (tok * G + g) * N, *vt = v + (tok * H + h) * P;
+                const double raw = dt_raw[tok * H + h] + dt_bias[h];
+                const double dt = raw > 0 ? raw + log1p(exp(-raw)) : log1p(exp(raw));
+                const double a = exp(-exp(A_log[h]) * dt);
+                const double beta = 1.0 / (1.0 + exp(-b_raw[tok * H + h]));
+                double kk = 1e-6, qq = 1e-6;
+                for (int n = 0; n < N; ++n) { kk += kt[n] * kt[n]; qq += qt[n] * qt[n]; }
+                const double rk = norm ? 1.0 / sqrt(kk) : 1.0, rq = norm ? 1.0 / sqrt(qq) : 1.0;
+                for (int p = 0; p < P; ++p) {
+                    double *s = S + (size_t)p * N, held = 0.0, acc = 0.0;
+                    for (int n = 0; n < N; ++n) held += a * s[n] * rk * kt[n];
+                    const double write = beta * (vt[p] - held);
+                    for (int n = 0; n < N; ++n) {
+                        s[n] = a * s[n] + write * rk * kt[n];
+                        acc += s[n] * rq * qt[n];
+                    }
+                    y[(tok * H + h) * P + p] = scale * acc;
+                }
+            }
+        }
+    return 0;
+}
+
+/*
+ * Grouped norm with a gate: rows of C channels in groups of D; kind 0: x /
+ * sqrt(mean(x^2) + eps), 1: (x - mean) / sqrt(variance + eps); times w plus b
+ * (C values, index c, or NULL); f(z) = z / (1 + exp(-z)) with act, else z;
+ * gate 0: f of the result, 1: result times f(z), 2: the norm of x f(z).
+ */
+int oracle_gated_norm(int rows, int C, int D, int kind, int gate, int act, const double *x, const double *z,
+                      const double *w, const double *bias, double eps, double *y)
+{
+    if (rows < 0 || D <= 0 || C % D) return -1;
+    for (size_t i = 0; i < (size_t)rows * (C / D); ++i) {
+        const double *xi = x + i * D, *zi = z ? z + i * D : NULL;
+        double *yi = y + i * D, mean = 0.0, var = 0.0;
+        const int c0 = (int)(i % (C / D)) * D;
+        for (int c = 0; c < D; ++c) {
+            const double f = gate ? (act ? oracle_silu(zi[c]) : zi[c]) : 0.0;
+            yi[c] = gate == 2 ? xi[c] * f : xi[c];
+            mean += yi[c] / D;
+        }
+        if (kind == 0) mean = 0.0;
+        for (int c = 0; c < D; ++c) var += (yi[c] - mean) * (yi[c] - mean) / D;
+        for (int c = 0; c < D; ++c) {
+            const double n = (yi[c] - mean) / sqrt(var + eps) * (w ? w[c0 + c] : 1.0) + (bias ? bias[c0 + c] : 0.0);
+            if (gate == 1) yi[c] = n * (act ? oracle_silu(zi[c]) : zi[c]);
+            else yi[c] = gate == 0 && act ? oracle_silu(n) : n;
+        }
+    }
+    return 0;
+}

@@ -76,6 +76,15 @@ _lib.axon_ssd_workspace_bytes.restype = _sz
 _lib.axon_ssd_workspace_bytes.argtypes = [_i] * 6
 _lib.axon_ssd_scan_fwd.restype = _i
 _lib.axon_ssd_scan_fwd.argtypes = [_i] * 6 + [_vp] * 10 + [_i, _vp, _sz, _vp]
+_lib.axon_delta_workspace_bytes.restype = _sz
+_lib.axon_delta_workspace_bytes.argtypes = [_i] * 7
+_lib.axon_delta_scan_fwd.restype = _i
+_lib.axon_delta_scan_fwd.argtypes = ([_i] * 7 + [_vp, _i] * 3 + [_vp] * 6 + [ctypes.c_float, _i] +
+                                     [_vp] * 3 + [_sz, _vp])
+_lib.axon_delta_step.restype = _i
+_lib.axon_delta_step.argtypes = [_i] * 6 + [_vp, _i] * 3 + [_vp] * 4 + [ctypes.c_float, _i] + [_vp] * 3
+_lib.axon_gated_norm_fwd.restype = _i
+_lib.axon_gated_norm_fwd.argtypes = [_i] * 7 + [_vp, _i] * 2 + [_vp] * 2 + [_i, ctypes.c_float, _vp, _i, _vp]
 _lib.axon_gemm_bf16.restype = _i
 _lib.axon_exp2_fma.restype = _i
 _lib.axon_peak_probe.restype = _i
@@ -292,6 +301,44 @@ def axon_ssd_scan_fwd(B, L, H, P, N, io, x, dt_raw, dt_bias, A_log, Bm, Cm, D, h
                                 int(workspace_bytes), _stream(stream))
     if raise_on_error:
         _check(rc, "axon_ssd_scan_fwd")
+    return rc
+
+
+def axon_delta_workspace_bytes(B, L, H, G, P=128, N=128, io=AXON_BF16) -> int:
+    return int(_lib.axon_delta_workspace_bytes(B, L, H, G, P, N, io))
+
+
+def _v(t):
+    """Device pointer of a tensor that may be a view with a row stride."""
+    return t if t is None or isinstance(t, int) else t.data_ptr()
+
+
+def axon_delta_scan_fwd(B, L, H, G, P, N, io, q, ldq, k, ldk, v, ldv, dt_raw, b_raw, dt_bias, A_log, lengths, h0,
+                        scale, qk_norm, y, h_out, workspace, workspace_bytes, stream=None, *,
+                        raise_on_error=True) -> int:
+    rc = _lib.axon_delta_scan_fwd(B, L, H, G, P, N, io, _v(q), ldq, _v(k), ldk, _v(v), ldv, _p(dt_raw), _p(b_raw),
+                                  _p(dt_bias), _p(A_log), _p(lengths), _p(h0), scale, qk_norm, _p(y), _p(h_out),
+                                  _p(workspace), int(workspace_bytes), _stream(stream))
+    if raise_on_error:
+        _check(rc, "axon_delta_scan_fwd")
+    return rc
+
+
+def axon_delta_step(B, H, G, P, N, io, q, ldq, k, ldk, v, ldv, dt_raw, b_raw, dt_bias, A_log, scale, qk_norm, state,
+                    y, stream=None, *, raise_on_error=True) -> int:
+    rc = _lib.axon_delta_step(B, H, G, P, N, io, _v(q), ldq, _v(k), ldk, _v(v), ldv, _p(dt_raw), _p(b_raw),
+                              _p(dt_bias), _p(A_log), scale, qk_norm, _p(state), _p(y), _stream(stream))
+    if raise_on_error:
+        _check(rc, "axon_delta_step")
+    return rc
+
+
+def axon_gated_norm_fwd(rows, C, D, io, kind, gate, act, x, ldx, z, ldz, weight, bias, per_channel, eps, y, ldy,
+                        stream=None, *, raise_on_error=True) -> int:
+    rc = _lib.axon_gated_norm_fwd(rows, C, D, io, kind, gate, act, _v(x), ldx, _v(z), ldz, _p(weight), _p(bias),
+                                  per_channel, eps, _v(y), ldy, _stream(stream))
+    if raise_on_error:
+        _check(rc, "axon_gated_norm_fwd")
     return rc
 
 
@@ -562,3 +609,194 @@ def ssd_scan(x, dt_raw, Bm, Cm, params: dict, h0=None, *, out=None, workspace=No
     if check and L > 0 and Bsz * H > 0 and ssd_error_flag(workspace) != 0:
         raise AxonError(6, "axon_ssd_scan_fwd (a wait for a tensor-core product gave up)")
     return y, h_out
+
+
+# ------------------------------------------------------------ gated delta rule, grouped norm
+def _same_device(what, dev, **tensors):
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: the inputs are on {dev}; a CUDA device is needed")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{what}: {name} is on {t.device}, not on {dev}")
+
+
+def _like(what, dtype, **tensors):
+    for name, (t, shape, *kind) in tensors.items():
+        if t is None:
+            continue
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        want = kind[0] if kind else dtype
+        if t.dtype != want:
+            raise TypeError(f"{what}: {name} is {t.dtype}, not {want}")
+
+
+def _token_stride(what, name, t):
+    """Elements between consecutive tokens of a (B, L, heads, D) or (B, heads,
+    D) tensor whose heads are dense and whose tokens lie at one stride (a slice
+    of a projected row, say)."""
+    heads, d = t.shape[-2:]
+    ld, n = heads * d, 1
+    for i in range(t.dim() - 3, -1, -1):
+        if t.shape[i] > 1 and n == 1:
+            ld, n = t.stride(i), t.shape[i]
+        elif t.shape[i] > 1:
+            if t.stride(i) != ld * n:
+                raise ValueError(f"{what}: the tokens of {name} do not lie at one stride")
+            n *= t.shape[i]
+    if (d > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != d):
+        raise ValueError(f"{what}: the heads of {name} must be dense")
+    return ld
+
+
+def _used_on(stream, dev, *tensors):
+    """Tells the allocator that tensors made here are used on another stream
+    than the current one, so their memory is not handed out while it is read."""
+    if stream is None:
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
+
+
+def _delta_args(what, q, k, v, dt_raw, b_raw, params, scale):
+    H, P = v.shape[-2:]
+    G, N = k.shape[-2:]
+    io = _dtype_code(v.dtype)
+    lead = tuple(v.shape[:-2])
+    dev = v.device
+    _same_device(what, dev, q=q, k=k, dt_raw=dt_raw, b_raw=b_raw, dt_bias=params["dt_bias"], A_log=params["A_log"])
+    f32 = torch.float32
+    _like(what, v.dtype, q=(q, lead + (G, N)), k=(k, lead + (G, N)), dt_raw=(dt_raw, lead + (H,)),
+          b_raw=(b_raw, lead + (H,)), dt_bias=(params["dt_bias"], (H,), f32), A_log=(params["A_log"], (H,), f32))
+    return H, P, G, N, io, (q, _token_stride(what, "q", q), k, _token_stride(what, "k", k), v,
+                            _token_stride(what, "v", v), dt_raw, b_raw, params["dt_bias"], params["A_log"]), \
+        (N ** -0.5 if scale is None else float(scale))
+
+
+def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, scale=None, qk_norm=True, out=None,
+               workspace=None, stream=None, check=True):
+    """Gated delta rule prefill: q, k (B,L,G,N), v (B,L,H,P), dt_raw, b_raw
+    (B,L,H); ``params`` holds dt_bias, A_log (H,) float32.  Returns
+    ``(y (B,L,H,P), h_out (B,H,P,N))``, h_out ready for the next call or for
+    ``delta_step``.
+
+    q, k and v may be slices of one projected row (dense heads, tokens at one
+    stride).  ``lengths`` ((B,) int32 on the device) ends rows early: y behind
+    a row's end is left as it was (undefined where y is allocated here).
+    ``scale`` defaults to N^(-1/2).  ``out`` = (y, h_out); h_out may be h0.
+    With ``check`` the call waits for the device and raises AxonError
+    (AXON_ERR_TIMEOUT) if a wait of the kernel gave up; ``check=False`` returns
+    at once (read the flag with ``delta_error_flag(workspace)``).
+    """
+    Bsz, L = v.shape[:2]
+    H, P, G, N, io, args, scale = _delta_args("delta_scan", q, k, v, dt_raw, b_raw, params, scale)
+    dev = v.device
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return delta_scan(q, k, v, dt_raw, b_raw, params, h0, lengths=lengths, scale=scale, qk_norm=qk_norm,
+                              out=out, workspace=workspace, stream=stream, check=check)
+    made = []
+    if out is None:
+        y = torch.empty(Bsz, L, H, P, dtype=v.dtype, device=dev)
+        h_out = torch.empty(Bsz, H, P, N, dtype=torch.float32, device=dev)
+        made += [y, h_out]
+    else:
+        y, h_out = out
+    _same_device("delta_scan", dev, h0=h0, lengths=lengths, y=y, h_out=h_out, workspace=workspace)
+    state = (Bsz, H, P, N)
+    _like("delta_scan", torch.float32, h0=(h0, state), h_out=(h_out, state), y=(y, v.shape, v.dtype),
+          lengths=(lengths, (Bsz,), torch.int32))
+    if workspace is None:
+        nbytes = axon_delta_workspace_bytes(Bsz, L, H, G, P, N, io)
+        if nbytes > 0:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            made.append(workspace)
+    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    axon_delta_scan_fwd(Bsz, L, H, G, P, N, io, *args, lengths, h0, scale, int(qk_norm), y, h_out, workspace, wsz,
+                        stream=stream)
+    _used_on(stream, dev, *made)
+    return y, h_out
+
+
+def delta_step(q, k, v, dt_raw, b_raw, params: dict, state, *, scale=None, qk_norm=True, y=None, stream=None):
+    """One cached step of the gated delta rule: q, k (B,G,N), v (B,H,P),
+    dt_raw, b_raw (B,H); ``state`` (B,H,P,N) float32 is updated in place.
+    Returns y (B,H,P)."""
+    Bsz = v.shape[0]
+    H, P, G, N, io, args, scale = _delta_args("delta_step", q, k, v, dt_raw, b_raw, params, scale)
+    dev = v.device
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return delta_step(q, k, v, dt_raw, b_raw, params, state, scale=scale, qk_norm=qk_norm, y=y, stream=stream)
+    made = y is None
+    if made:
+        y = torch.empty(Bsz, H, P, dtype=v.dtype, device=dev)
+    _same_device("delta_step", dev, state=state, y=y)
+    _like("delta_step", torch.float32, state=(state, (Bsz, H, P, N)), y=(y, (Bsz, H, P), v.dtype))
+    axon_delta_step(Bsz, H, G, P, N, io, *args, scale, int(qk_norm), state, y, stream=stream)
+    if made:
+        _used_on(stream, dev, y)
+    return y
+
+
+NORM_KINDS = {"rms": 0, "group": 1}
+NORM_GATES = {"after": 1, "before": 2}
+
+
+def _row_stride(what, name, t, rows, C):
+    """(elements between the rows) of a (..., C) tensor whose rows lie at one stride."""
+    t2 = t.view(rows, C) if t.is_contiguous() or t.dim() == 2 else None
+    if t2 is None:
+        ld, n = C, 1
+        for i in range(t.dim() - 2, -1, -1):
+            if t.shape[i] > 1 and n == 1:
+                ld, n = t.stride(i), t.shape[i]
+            elif t.shape[i] > 1:
+                if t.stride(i) != ld * n:
+                    raise ValueError(f"{what}: the rows of {name} do not lie at one stride")
+                n *= t.shape[i]
+    else:
+        ld = t2.stride(0) if rows > 1 else C
+    if C > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: the channels of {name} must be dense")
+    return ld
+
+
+def gated_norm(x, weight=None, z=None, *, bias=None, group=None, kind="rms", gate="after", act=True, eps=1e-6,
+               out=None, stream=None):
+    """Grouped norm of channels-last rows x (..., C) with a SiLU gate or
+    activation: statistics per row and ``group`` channels (default C).
+
+    ``kind``: "rms" or "group" (mean and variance).  With z (same shape):
+    ``gate`` "after" gives norm(x) f(z), "before" the norm of x f(z); without
+    z the result is f(norm(x)).  f is SiLU with ``act``, else the identity.
+    weight, bias: float32, (group,) shared by the groups or (C,); both of one
+    form.  x, z and out may be slices with a row stride; out may be x or z.
+    """
+    C = x.shape[-1]
+    D = C if group is None else int(group)
+    dev = x.device
+    _same_device("gated_norm", dev)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gated_norm(x, weight, z, bias=bias, group=group, kind=kind, gate=gate, act=act, eps=eps, out=out,
+                              stream=stream)
+    made = out is None
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if made else out
+    _same_device("gated_norm", dev, weight=weight, bias=bias, z=z, out=y)
+    forms = {t.numel() for t in (weight, bias) if t is not None}
+    if len(forms) > 1 or not forms <= {D, C}:
+        raise ValueError(f"gated_norm: weight and bias need {D} or {C} values, both the same")
+    n = forms.pop() if forms else D
+    _like("gated_norm", torch.float32, weight=(weight, (n,)), bias=(bias, (n,)), z=(z, x.shape, x.dtype),
+          out=(y, x.shape, x.dtype))
+    rows = x.numel() // C if C else 0
+    axon_gated_norm_fwd(rows, C, D, _dtype_code(x.dtype), NORM_KINDS[kind], NORM_GATES[gate] if z is not None else 0,
+                        int(act), x, _row_stride("gated_norm", "x", x, rows, C), z,
+                        0 if z is None else _row_stride("gated_norm", "z", z, rows, C), weight, bias,
+                        int(n == C and n != D), eps, y, _row_stride("gated_norm", "out", y, rows, C), stream=stream)
+    if made:
+        _used_on(stream, dev, y)
+    return y

@@ -1,0 +1,217 @@
+// axon_delta.cu -- C ABI of the gated delta rule and of the grouped gated norm
+// (include/axon_ssm.h): argument checks, launch plans, launches of
+// delta_step.cuh and gated_norm.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "axon_ssm.h"
+#include "delta_step.cuh"
+#include "gated_norm.cuh"
+
+namespace axon {
+namespace {
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool ovl(const void* a, size_t na, const void* b, size_t nb) {
+    if (!a || !b || na == 0 || nb == 0) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + nb && b0 < a0 + na;
+}
+// bytes from the first to behind the last value of `rows` rows of `cols` values, ld apart
+size_t extent(size_t rows, size_t cols, size_t ld, size_t es) { return rows ? ((rows - 1) * ld + cols) * es : 0; }
+
+// Whether two sets of `rows` rows of `cols` values overlap; rows of one stride
+// may interleave (slices of one wider row).
+bool rows_ovl(const void* a, size_t lda, const void* b, size_t ldb, size_t rows, size_t cols, size_t es) {
+    if (!ovl(a, extent(rows, cols, lda, es), b, extent(rows, cols, ldb, es))) return false;
+    if (lda != ldb) return true;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    const size_t d = (a0 < b0 ? b0 - a0 : a0 - b0) % (lda * es);
+    return d < cols * es || d + cols * es > lda * es;
+}
+
+int sm_count() {
+    static std::atomic<int> cached[64];   // zero-initialised (static storage)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 148;
+    if (dev < 64) {
+        const int v = cached[dev].load(std::memory_order_relaxed);
+        if (v > 0) return v;
+    }
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+bool shape_ok(int H, int G, int P, int N) {
+    return G > 0 && H % G == 0 && (P == 64 || P == 128) && (N == 64 || N == 128);
+}
+
+// What both delta entry points check alike; `rows` = tokens of all sequences.
+axon_status check_delta(size_t rows, int H, int G, int P, int N, axon_dtype io, const void* q, int ldq, const void* k,
+                        int ldk, const void* v, int ldv, const void* dt_raw, const void* b_raw, const float* dt_bias,
+                        const float* A_log, float scale) {
+    if (!shape_ok(H, G, P, N) || (io != AXON_F32 && io != AXON_BF16)) return AXON_ERR_UNSUPPORTED;
+    if (!dt_bias || !A_log || !std::isfinite(scale)) return AXON_ERR_INVALID_ARG;
+    if (rows > 0 && (!q || !k || !v || !dt_raw || !b_raw)) return AXON_ERR_INVALID_ARG;
+    if (ldq < G * N || ldk < G * N || ldv < H * P) return AXON_ERR_INVALID_ARG;
+    const int m = io == AXON_BF16 ? 8 : 4;
+    if (ldq % m || ldk % m || ldv % m) return AXON_ERR_ALIGNMENT;
+    for (const void* t : {q, k, v, dt_raw, b_raw, (const void*)dt_bias, (const void*)A_log})
+        if (t && !al16(t)) return AXON_ERR_ALIGNMENT;
+    return AXON_OK;
+}
+
+template <class Io, int N>
+void launch_step(const DeltaParams& p, cudaStream_t st) {
+    constexpr int ROWS1 = 4 * (32 / (N / 16));                      // rows of a block at RT = 1
+    // Four rows a lane keep more loads in flight (one row each leaves a third
+    // of the bandwidth unused on a large batch); below two blocks an SM that
+    // way, the rows are spread over more blocks.
+    constexpr int RT = N == 128 ? 4 : 2;
+    if ((long long)p.B * p.H * (p.P / (ROWS1 * RT)) >= 2LL * sm_count())
+        delta_step_kernel<Io, N, RT><<<dim3((unsigned)(p.P / (ROWS1 * RT)), (unsigned)p.H, (unsigned)p.B), 128, 0, st>>>(p);
+    else
+        delta_step_kernel<Io, N, 1><<<dim3((unsigned)(p.P / ROWS1), (unsigned)p.H, (unsigned)p.B), 128, 0, st>>>(p);
+}
+template <class Io, int N>
+void launch_recur(const DeltaParams& p, cudaStream_t st) {
+    constexpr int ROWS1 = 4 * (32 / (N / 16));
+    constexpr int RT = N == 128 ? 4 : 2;
+    if ((long long)p.B * p.H * (p.P / (ROWS1 * RT)) >= sm_count())
+        delta_recur_kernel<Io, N, RT><<<dim3((unsigned)(p.P / (ROWS1 * RT)), (unsigned)p.H, (unsigned)p.B), 128, 0, st>>>(p);
+    else
+        delta_recur_kernel<Io, N, 1><<<dim3((unsigned)(p.P / ROWS1), (unsigned)p.H, (unsigned)p.B), 128, 0, st>>>(p);
+}
+
+// Lanes a group and pieces a lane: the fewest lanes (4 .. 32) that hold the
+// group in one piece each, then more pieces, then whole blocks.
+template <class Io>
+void launch_norm(const NormParams& p, cudaStream_t st) {
+    const int pieces = p.D / NormVec<Io>::VE;
+    auto warps = [&](auto kernel, int LG, int U) {
+        const int per_block = 8 * (32 / LG) * U;
+        kernel<<<(unsigned)((p.groups + per_block - 1) / per_block), 256, 0, st>>>(p);
+    };
+    if (pieces <= 4) warps(gated_norm_kernel<Io, 4, 1, 4, 1>, 4, 4);
+    else if (pieces <= 8) warps(gated_norm_kernel<Io, 8, 1, 4, 1>, 8, 4);
+    else if (pieces <= 16) warps(gated_norm_kernel<Io, 16, 1, 4, 1>, 16, 4);
+    else if (pieces <= 32) warps(gated_norm_kernel<Io, 32, 1, 4, 1>, 32, 4);
+    else if (pieces <= 64) warps(gated_norm_kernel<Io, 32, 2, 2, 1>, 32, 2);
+    else if (pieces <= 128) warps(gated_norm_kernel<Io, 32, 4, 1, 1>, 32, 1);
+    else if (pieces <= 512) gated_norm_kernel<Io, 32, 2, 1, 8><<<(unsigned)p.groups, 256, 0, st>>>(p);
+    else if (pieces <= 1024) gated_norm_kernel<Io, 32, 4, 1, 8><<<(unsigned)p.groups, 256, 0, st>>>(p);
+    else gated_norm_kernel<Io, 32, 8, 1, 8><<<(unsigned)p.groups, 256, 0, st>>>(p);
+}
+
+}  // namespace
+}  // namespace axon
+
+using namespace axon;
+
+extern "C" {
+
+size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io) {
+    (void)B; (void)L; (void)H; (void)G; (void)P; (void)N; (void)io;
+    return 0;
+}
+
+axon_status axon_delta_scan_fwd(int B, int L, int H, int G, int P, int N, axon_dtype io,
+                                const void* q, int ldq, const void* k, int ldk, const void* v, int ldv,
+                                const void* dt_raw, const void* b_raw, const float* dt_bias, const float* A_log,
+                                const int* lengths, const float* h0, float scale, int qk_norm,
+                                void* y, float* h_out, void* workspace, size_t workspace_bytes,
+                                axon_stream_t stream) {
+    if (B < 0 || L < 0 || H < 0) return AXON_ERR_INVALID_ARG;
+    if (B > 65535 || H > 65535 || (long long)B * L * H > (1LL << 31)) return AXON_ERR_UNSUPPORTED;
+    if (B == 0 || H == 0) return AXON_OK;
+    const size_t rows = (size_t)B * L;
+    const axon_status rc = check_delta(rows, H, G, P, N, io, q, ldq, k, ldk, v, ldv, dt_raw, b_raw, dt_bias, A_log, scale);
+    if (rc != AXON_OK) return rc;
+    if (!h_out || (rows > 0 && !y)) return AXON_ERR_INVALID_ARG;
+    if (!al16(y) || !al16(h_out) || !al16(h0) || !al16(workspace) || (reinterpret_cast<uintptr_t>(lengths) & 3u))
+        return AXON_ERR_ALIGNMENT;
+    const size_t n_ws = axon_delta_workspace_bytes(B, L, H, G, P, N, io);
+    if (workspace_bytes < n_ws) return AXON_ERR_WORKSPACE;
+    if (n_ws > 0 && !workspace) return AXON_ERR_INVALID_ARG;
+    const size_t es = io == AXON_BF16 ? 2 : 4;
+    const size_t n_h = (size_t)B * H * P * N * 4, n_y = rows * H * P * es, n_g = rows * H * es;
+    const struct { const void* p; size_t n; } in[] = {
+        {q, extent(rows, (size_t)G * N, ldq, es)}, {k, extent(rows, (size_t)G * N, ldk, es)},
+        {v, extent(rows, (size_t)H * P, ldv, es)}, {dt_raw, n_g}, {b_raw, n_g},
+        {dt_bias, (size_t)H * 4}, {A_log, (size_t)H * 4}, {lengths, (size_t)B * 4}};
+    for (const auto& t : in)
+        if (ovl(t.p, t.n, y, n_y) || ovl(t.p, t.n, h_out, n_h) || ovl(t.p, t.n, workspace, n_ws)) return AXON_ERR_INVALID_ARG;
+    if (ovl(h0, n_h, y, n_y) || ovl(h0, n_h, workspace, n_ws) || ovl(h_out, n_h, y, n_y) ||
+        ovl(h_out, n_h, workspace, n_ws) || ovl(y, n_y, workspace, n_ws))
+        return AXON_ERR_INVALID_ARG;
+    if (h0 != h_out && ovl(h0, n_h, h_out, n_h)) return AXON_ERR_INVALID_ARG;
+
+    DeltaParams p{B, L, H, G, P, ldq, ldk, ldv, q, k, v, dt_raw, b_raw, dt_bias, A_log, lengths, h0, y, h_out, scale, qk_norm != 0};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (io == AXON_BF16) N == 128 ? launch_recur<IoBF16, 128>(p, st) : launch_recur<IoBF16, 64>(p, st);
+    else N == 128 ? launch_recur<IoF32, 128>(p, st) : launch_recur<IoF32, 64>(p, st);
+    return cudaGetLastError() == cudaSuccess ? AXON_OK : AXON_ERR_CUDA;
+}
+
+axon_status axon_delta_step(int B, int H, int G, int P, int N, axon_dtype io,
+                            const void* q, int ldq, const void* k, int ldk, const void* v, int ldv,
+                            const void* dt_raw, const void* b_raw, const float* dt_bias, const float* A_log,
+                            float scale, int qk_norm, float* state, void* y, axon_stream_t stream) {
+    if (B < 0 || H < 0) return AXON_ERR_INVALID_ARG;
+    if (B > 65535 || H > 65535) return AXON_ERR_UNSUPPORTED;
+    if (B == 0 || H == 0) return AXON_OK;
+    const axon_status rc = check_delta((size_t)B, H, G, P, N, io, q, ldq, k, ldk, v, ldv, dt_raw, b_raw, dt_bias, A_log, scale);
+    if (rc != AXON_OK) return rc;
+    if (!state || !y) return AXON_ERR_INVALID_ARG;
+    if (!al16(state) || !al16(y)) return AXON_ERR_ALIGNMENT;
+    const size_t es = io == AXON_BF16 ? 2 : 4, n_h = (size_t)B * H * P * N * 4, n_y = (size_t)B * H * P * es;
+    const struct { const void* p; size_t n; } in[] = {
+        {q, extent(B, (size_t)G * N, ldq, es)}, {k, extent(B, (size_t)G * N, ldk, es)},
+        {v, extent(B, (size_t)H * P, ldv, es)}, {dt_raw, (size_t)B * H * es}, {b_raw, (size_t)B * H * es},
+        {dt_bias, (size_t)H * 4}, {A_log, (size_t)H * 4}};
+    for (const auto& t : in)
+        if (ovl(t.p, t.n, y, n_y) || ovl(t.p, t.n, state, n_h)) return AXON_ERR_INVALID_ARG;
+    if (ovl(state, n_h, y, n_y)) return AXON_ERR_INVALID_ARG;
+
+    DeltaParams p{B, 1, H, G, P, ldq, ldk, ldv, q, k, v, dt_raw, b_raw, dt_bias, A_log, nullptr, state, y, state, scale, qk_norm != 0};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (io == AXON_BF16) N == 128 ? launch_step<IoBF16, 128>(p, st) : launch_step<IoBF16, 64>(p, st);
+    else N == 128 ? launch_step<IoF32, 128>(p, st) : launch_step<IoF32, 64>(p, st);
+    return cudaGetLastError() == cudaSuccess ? AXON_OK : AXON_ERR_CUDA;
+}
+
+axon_status axon_gated_norm_fwd(int rows, int C, int D, axon_dtype io, axon_norm_kind kind, axon_norm_gate gate, int act,
+                                const void* x, int ldx, const void* z, int ldz, const float* weight, const float* bias,
+                                int per_channel, float eps, void* y, int ldy, axon_stream_t stream) {
+    if (rows < 0 || C < 0 || D <= 0 || C % D) return AXON_ERR_INVALID_ARG;
+    if ((io != AXON_F32 && io != AXON_BF16) || (kind != AXON_NORM_RMS && kind != AXON_NORM_GROUP) ||
+        (gate != AXON_GATE_NONE && gate != AXON_GATE_AFTER && gate != AXON_GATE_BEFORE))
+        return AXON_ERR_UNSUPPORTED;
+    if (D > 8192 || (long long)rows * (C / D) >= (1LL << 31)) return AXON_ERR_UNSUPPORTED;
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return AXON_ERR_INVALID_ARG;
+    if (rows == 0 || C == 0) return AXON_OK;
+    const bool gated = gate != AXON_GATE_NONE;
+    if (!x || !y || (gated && !z) || ldx < C || ldy < C || (gated && ldz < C)) return AXON_ERR_INVALID_ARG;
+    const int m = io == AXON_BF16 ? 8 : 4;
+    if (D % m || ldx % m || ldy % m || (gated && ldz % m)) return AXON_ERR_ALIGNMENT;
+    if (!al16(x) || !al16(y) || (gated && !al16(z)) || !al16(weight) || !al16(bias)) return AXON_ERR_ALIGNMENT;
+    const size_t es = io == AXON_BF16 ? 2 : 4, n_w = (size_t)(per_channel ? C : D) * 4, n_y = extent(rows, C, ldy, es);
+    if (!(y == x && ldy == ldx) && rows_ovl(x, ldx, y, ldy, rows, C, es)) return AXON_ERR_INVALID_ARG;
+    if (gated && !(y == z && ldy == ldz) && rows_ovl(z, ldz, y, ldy, rows, C, es)) return AXON_ERR_INVALID_ARG;
+    if (ovl(weight, n_w, y, n_y) || ovl(bias, n_w, y, n_y)) return AXON_ERR_INVALID_ARG;
+
+    NormParams p{rows, C, D, rows * (C / D), ldx, ldz, ldy, x, gated ? z : nullptr, weight, bias, per_channel != 0,
+                 kind == AXON_NORM_GROUP, gate == AXON_GATE_BEFORE, act != 0, eps, y};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (io == AXON_BF16) launch_norm<IoBF16>(p, st);
+    else launch_norm<IoF32>(p, st);
+    return cudaGetLastError() == cudaSuccess ? AXON_OK : AXON_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -29,6 +29,10 @@ dt_raw ~ N(0, 0.5), B, C ~ N(0, 1) (B,L,128) in bf16; per head dt_bias =
 log(expm1(u)), u ~ logUniform[1e-3, 1e-1], A_log = log(Uniform[1, 16]) and
 D = 1; an initial state h0 ~ N(0, 1/4).
 
+The gated delta rule workloads (``DELTA_WORKLOADS``): q, k, v = SiLU of N(0, 1)
+(what a causal convolution leaves), dt_raw ~ N(0, 0.5), b_raw ~ N(0, 1) in the
+io dtype; dt_bias and A_log as for SSD; an initial state h0 ~ N(0, 1/4).
+
 The whole-layer workloads (``BLOCK_WORKLOADS``) draw the layer input
 X ~ N(0, 1) and the projection weights with fan-in scaling, W_in ~ N(0, 1/Dm),
 W_x ~ N(0, 1/E), W_out ~ N(0, 1/E), all rounded to bf16 once; the per-channel
@@ -261,3 +265,49 @@ def make_ssd_inputs(sw: SsdWorkload, with_state: bool = False, L: int | None = N
     if with_state:
         out["h0"] = torch.randn(B, H, P, N, generator=g, dtype=torch.float32) * 0.5
     return out
+
+
+# ------------------------------------------------------------ gated delta rule
+@dataclass(frozen=True)
+class DeltaWorkload:
+    name: str
+    B: int
+    L: int
+    G: int           # key heads
+    H: int           # value heads
+    seed: int
+    P: int = 128
+    N: int = 128
+    io: str = "bf16"
+    note: str = ""
+
+
+DELTA_WORKLOADS = [
+    DeltaWorkload("delta_layer", 1, 4096, 16, 32, 31,
+                  note="32 value heads of 128 on 16 key heads of 128, bf16"),
+    DeltaWorkload("small_delta", 2, 130, 2, 4, 32, note="small case for parity tests"),
+]
+DELTA_WORKLOAD_BY_NAME = {w.name: w for w in DELTA_WORKLOADS}
+
+
+def make_delta_inputs(dw: DeltaWorkload, L: int | None = None, B: int | None = None) -> dict:
+    """q, k (B,L,G,N), v (B,L,H,P), dt_raw, b_raw (B,L,H), dt_bias, A_log (H),
+    h0 (B,H,P,N), on the CPU."""
+    g = _gen(dw.seed + 9000)
+    L = dw.L if L is None else L
+    B = dw.B if B is None else B
+    G, H, P, N = dw.G, dw.H, dw.P, dw.N
+    io = torch.float32 if dw.io == "f32" else torch.bfloat16
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, dtype=torch.float32)
+
+    silu = torch.nn.functional.silu
+    u = torch.exp(math.log(1e-3) + math.log(1e2) * torch.rand(H, generator=g, dtype=torch.float64))
+    return {
+        "q": silu(normal(B, L, G, N)).to(io), "k": silu(normal(B, L, G, N)).to(io), "v": silu(normal(B, L, H, P)).to(io),
+        "dt_raw": (normal(B, L, H) * math.sqrt(0.5)).to(io), "b_raw": normal(B, L, H).to(io),
+        "dt_bias": torch.log(torch.expm1(u)).to(torch.float32),
+        "A_log": torch.log(1.0 + 15.0 * torch.rand(H, generator=g, dtype=torch.float64)).to(torch.float32),
+        "h0": normal(B, H, P, N) * 0.5,
+    }

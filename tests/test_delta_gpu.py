@@ -1,0 +1,316 @@
+"""GPU parity of the gated delta rule (prefill and cached step) against the
+fp64 oracle on the same inputs.
+
+Tolerances, set before the first run (u = 2^-24, the float32 half step):
+  * float32 y and every state, token-by-token kernel: an update costs a handful
+    of roundings (u each) and gates exact to a few 2^-22; the map
+    a (I - beta k k^T) never lengthens a state row, so errors add up over the
+    memory's horizon at worst: normwise 1e-5.
+  * state of the chunked kernel: the same arithmetic in another order, with
+    operands in two fp16 parts (2^-22 of a row's largest value dropped, at most),
+    amplified by a chunk's triangular factor (its norm measured up to 8):
+    normwise 8 * 2^-22 * sqrt(5 products) = 4.3e-6, and the tensor cores' own
+    float32 sums: asserted at 1e-5 too.
+  * bf16 y: the output rounding (half a step: 2^-8 of the value at worst, so at
+    most 2^-8 / sqrt(3) = 2.3e-3 rms) and three operands rounded to one fp16
+    part (2^-11 each): normwise 2.6e-3; elementwise 5 sigma of that against
+    the head's rms: 1.3e-2 * max(rms, |ref|).
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from selective_state_space_52_b200 import workloads as W
+
+from gpu_util import Guarded
+
+pytestmark = pytest.mark.gpu
+
+SEQ = ("q", "k", "v", "dt_raw", "b_raw")
+
+
+def close(got, ref, norm_tol, what, elem=None):
+    got, ref = (np.asarray(t, dtype=np.float64) for t in (got, ref))
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    assert np.all(np.isfinite(got)), what + ": non-finite"
+    rel = np.linalg.norm(got - ref) / max(np.linalg.norm(ref), 1e-30)
+    assert rel <= norm_tol, f"{what}: normwise {rel:.3g}"
+    rms = np.sqrt(np.mean(ref * ref)) if ref.size else 0.0
+    off = np.abs(got - ref) / np.maximum(max(rms, 1e-30), np.abs(ref)) if ref.size else np.zeros(1)
+    elem = 40 * norm_tol if elem is None else elem
+    assert off.max() <= elem, f"{what}: an element is {off.max():.3g} off"
+
+
+def tols(io):
+    return (1e-5, None) if io == "f32" else (2.6e-3, 1.3e-2)
+
+
+def make(N=128, P=128, G=2, H=4, io="bf16", L=130, B=2, seed=32):
+    return W.make_delta_inputs(W.DeltaWorkload("t", B, L, G, H, seed, P, N, io))
+
+
+def dev(inp):
+    d = {k: v.cuda() for k, v in inp.items()}
+    return d, {"dt_bias": d["dt_bias"], "A_log": d["A_log"]}
+
+
+def run(inp, h0=True, lengths=None, in_place=False, **kw):
+    from selective_state_space_52_b200 import axon_ssm
+    d, params = dev(inp)
+    B, L, H, P = d["v"].shape
+    N = d["k"].shape[-1]
+    gy, gh = Guarded((B, L, H, P), d["v"].dtype), Guarded((B, H, P, N), torch.float32)
+    gy.t.fill_(7.0)
+    h = d["h0"] if h0 else None
+    if in_place:
+        gh.t.copy_(h)
+        h = gh.t
+    ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    axon_ssm.delta_scan(*(d[k] for k in SEQ), params, h, lengths=ln, out=(gy.t, gh.t), **kw)
+    torch.cuda.synchronize()
+    assert gy.canaries_intact() and gh.canaries_intact()
+    return gy.t.float().cpu().numpy(), gh.t.cpu().numpy()
+
+
+def ref(inp, h0=True, lengths=None, qk_norm=True, scale=None):
+    return oracle.delta_scan(*(inp[k] for k in SEQ), inp["dt_bias"], inp["A_log"], inp["h0"] if h0 else None,
+                             lengths, scale, qk_norm)
+
+
+def check(inp, what, state_tol=1e-5, **kw):
+    y, h = run(inp, **kw)
+    kw.pop("in_place", None)
+    y_ref, h_ref = ref(inp, **kw)
+    io = "f32" if inp["v"].dtype == torch.float32 else "bf16"
+    ln = kw.get("lengths")
+    if ln is not None:
+        for b, n in enumerate(ln):
+            n = min(max(n, 0), y.shape[1])
+            assert np.all(y[b, n:] == 7.0), f"{what}: y behind the end of row {b} was written"
+            y_ref[b, n:] = 7.0
+    if y.size:
+        close(y, y_ref, tols(io)[0], what + " y", tols(io)[1])
+    close(h, h_ref, state_tol, what + " state")
+
+
+@pytest.mark.parametrize("L", [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 200, 333])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_lengths(cuda_lib, L, io):
+    inp = make(L=L, io=io)
+    check(inp, f"L{L} {io}")
+    check(inp, f"L{L} {io} no h0", h0=False)
+
+
+@pytest.mark.parametrize("N, P", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("G, H", [(1, 1), (1, 3), (2, 2), (3, 12)])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_heads(cuda_lib, N, P, G, H, io):
+    check(make(N, P, G, H, io, L=100, B=1), f"N{N} P{P} G{G} H{H} {io}")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_many_blocks(cuda_lib, io):
+    """Enough heads that every block keeps the most rows a lane holds."""
+    check(make(G=16, H=32, B=5, L=70, io=io), "B5 H32 " + io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("kw", [dict(qk_norm=False), dict(scale=1.0), dict(scale=-0.3, qk_norm=False)])
+def test_norm_and_scale(cuda_lib, io, kw):
+    inp = make(L=150, io=io)
+    if not kw.get("qk_norm", True):
+        for n in ("q", "k"):
+            t = inp[n].float()
+            inp[n] = (t / t.norm(dim=-1, keepdim=True)).to(inp[n].dtype)
+    check(inp, str(kw), **kw)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_ragged_rows(cuda_lib, io):
+    """Rows of every kind of length; what lies behind a row's end is NaN and
+    infinity, and y there stays as it was."""
+    lengths = [0, 1, 63, 64, 65, 130, 150, 400, -3]                 # the last two are taken into 0 .. L
+    inp = make(B=len(lengths), L=150, io=io)
+    dirty = {k: v.clone() for k, v in inp.items()}
+    for b, n in enumerate(lengths):
+        n = min(max(n, 0), 150)
+        for i, name in enumerate(SEQ):
+            dirty[name][b, n:] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+            inp[name][b, n:] = 0
+    y, h = run(dirty, lengths=lengths)
+    y_ref, h_ref = ref(inp, lengths=lengths)
+    for b, n in enumerate(lengths):
+        n = min(max(n, 0), 150)
+        assert np.all(y[b, n:] == 7.0), b
+        if n:
+            close(y[b, :n], y_ref[b, :n], tols(io)[0], f"y of row {b}", tols(io)[1])
+        close(h[b], h_ref[b], 1e-5, f"state of row {b}")
+        if n == 0:
+            np.testing.assert_array_equal(h[b], inp["h0"][b].numpy())
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [0, 40, 300])
+def test_state_in_place(cuda_lib, io, L):
+    check(make(L=L, io=io), f"in place L{L}", in_place=True)
+
+
+@pytest.mark.parametrize("L", [40, 300])
+def test_slices_of_one_projection(cuda_lib, L):
+    """q, k and v as slices of one row (tokens at the row's stride), bit for
+    bit what dense tensors give."""
+    from selective_state_space_52_b200 import axon_ssm
+    d, params = dev(make(L=L, B=2, G=2, H=4))
+    rowed = torch.cat([torch.full((2, L, 8), float("nan"), device="cuda", dtype=torch.bfloat16)] +
+                      [d[n].flatten(2) for n in ("q", "k", "v")] +
+                      [torch.full((2, L, 24), float("nan"), device="cuda", dtype=torch.bfloat16)], dim=-1)
+    q = rowed[..., 8:264].unflatten(-1, (2, 128))
+    k = rowed[..., 264:520].unflatten(-1, (2, 128))
+    v = rowed[..., 520:1032].unflatten(-1, (4, 128))
+    y, h = axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"])
+    y2, h2 = axon_ssm.delta_scan(q, k, v, d["dt_raw"], d["b_raw"], params, d["h0"])
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+
+
+def extreme(io, L=200):
+    """Head 0 forgets nothing (dt underflows to a decay of 1), head 1 forgets
+    all (decay 0 within a token), head 2 writes nothing (beta 0), head 3 takes
+    one large jump in a slow decay; keys of both key heads partly repeated, a
+    zero key and a zero query among them."""
+    inp = make(io=io, L=L, B=1)
+    inp["dt_bias"][:] = torch.tensor([-60.0, 80.0, -3.0, -6.0])
+    inp["A_log"][:] = torch.tensor([0.0, 2.7, 1.0, 0.0])
+    inp["b_raw"][:, :, 2] = -200.0
+    inp["b_raw"][:, 50:60] = 90.0
+    inp["dt_raw"][:, 100, 3] = 300.0
+    inp["k"][:, 20:90] = inp["k"][:, 20:21]
+    inp["k"][:, 130] = 0.0
+    inp["q"][:, 131] = 0.0
+    return inp
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_extreme_gates(cuda_lib, io):
+    inp = extreme(io)
+    y, h = run(inp)
+    y_ref, h_ref = ref(inp)
+    for hd in range(4):
+        close(y[:, :, hd], y_ref[:, :, hd], tols(io)[0], f"y of head {hd}", tols(io)[1])
+        close(h[:, hd], h_ref[:, hd], 1e-5, f"state of head {hd}")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_infinite_gates(cuda_lib, io):
+    """dt_raw of +inf forgets everything, -inf nothing; b_raw likewise."""
+    inp = make(io=io, L=70, B=1)
+    want = {k: v.clone() for k, v in inp.items()}
+    for name, t, big in (("dt_raw", 10, 3e4), ("dt_raw", 20, -3e4), ("b_raw", 30, 3e4), ("b_raw", 40, -3e4)):
+        inp[name][:, t] = float("inf") if big > 0 else -float("inf")
+        want[name][:, t] = big
+    y, h = run(inp)
+    y_ref, h_ref = ref(want)
+    close(y, y_ref, tols(io)[0], "y", tols(io)[1])
+    close(h, h_ref, 1e-5, "state")
+
+
+def test_nan_gate_shows(cuda_lib):
+    """A NaN in a gate is not swallowed: its head's later outputs are NaN, the others' are not."""
+    inp = make(L=90, B=1)
+    inp["dt_raw"][0, 10, 1] = float("nan")
+    y, h = run(inp)
+    assert np.isnan(y[0, 64:, 1]).all() and np.isnan(h[0, 1]).all()
+    assert np.isfinite(y[0, :, [0, 2, 3]]).all() and np.isfinite(h[0, [0, 2, 3]]).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_two_calls_and_streams_agree(cuda_lib, io):
+    """Back-to-back calls on one workspace, a call on another stream and a
+    captured graph replayed twice: bit for bit the same."""
+    from selective_state_space_52_b200 import axon_ssm
+    d, params = dev(make(L=300, io=io))
+    other, _ = dev(make(L=300, io=io, seed=77))
+    B, L, H, P = d["v"].shape
+    io_code = axon_ssm.AXON_F32 if io == "f32" else axon_ssm.AXON_BF16
+    ws = torch.empty(max(16, axon_ssm.axon_delta_workspace_bytes(B, L, H, 2, P, 128, io_code)), dtype=torch.uint8, device="cuda")
+    y, h = axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"], workspace=ws)
+    axon_ssm.delta_scan(*(other[n] for n in SEQ), params, other["h0"], workspace=ws, check=False)
+    y2, h2 = axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"], workspace=ws)
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y3, h3 = axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"], stream=side, check=False)
+    side.synchronize()
+    assert torch.equal(y, y3) and torch.equal(h, h3)
+    out = torch.zeros_like(y), torch.zeros_like(h)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"], workspace=ws, out=out, check=False)
+    for _ in range(2):
+        out[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, out[0]) and torch.equal(h, out[1])
+
+
+# ------------------------------------------------------------ the cached step
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N, P", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("B, G, H", [(1, 1, 1), (3, 2, 6), (40, 4, 16)])
+def test_step(cuda_lib, io, N, P, B, G, H):
+    from selective_state_space_52_b200 import axon_ssm
+    inp = make(N, P, G, H, io, L=1, B=B)
+    d, params = dev(inp)
+    st = Guarded((B, H, P, N), torch.float32, fill=d["h0"])
+    gy = Guarded((B, H, P), d["v"].dtype)
+    axon_ssm.delta_step(*(d[n][:, 0] for n in ("q", "k", "v")), *(d[n][:, 0].contiguous() for n in ("dt_raw", "b_raw")),
+                        params, st.t, y=gy.t)
+    torch.cuda.synchronize()
+    assert st.canaries_intact() and gy.canaries_intact()
+    y_ref, h_ref = ref(inp)
+    close(gy.t.float().cpu().numpy(), y_ref[:, 0], tols(io)[0], "y", tols(io)[1])
+    close(st.t.cpu().numpy(), h_ref, 1e-5, "state")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_step_extremes(cuda_lib, io):
+    from selective_state_space_52_b200 import axon_ssm
+    inp = extreme(io)
+    for t in (0, 55, 100, 130, 131):
+        one = {k: (v[:, t:t + 1].contiguous() if k in SEQ else v) for k, v in inp.items()}
+        d, params = dev(one)
+        y = axon_ssm.delta_step(*(d[n][:, 0] for n in SEQ), params, d["h0"], qk_norm=False, scale=0.5)
+        y_ref, h_ref = ref(one, qk_norm=False, scale=0.5)
+        close(y.float().cpu().numpy(), y_ref[:, 0], tols(io)[0], f"y of token {t}", tols(io)[1])
+        close(d["h0"].cpu().numpy(), h_ref, 1e-5, f"state after token {t}")
+
+
+# ------------------------------------------------------------ together, as a program uses them
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_prefill_then_decode_then_norm(cuda_lib, io):
+    """A prompt in two pieces (the second continues the first), six decode
+    steps, the output norm with its gate on every token: against the oracle's
+    one run over the whole sequence."""
+    from selective_state_space_52_b200 import axon_ssm
+    L, cut, steps = 150, 83, 6
+    inp = make(L=L + steps, io=io)
+    d, params = dev(inp)
+    dt = d["v"].dtype
+    B, _, H, P = d["v"].shape
+    g = torch.Generator().manual_seed(5)
+    z = torch.randn(B, L + steps, H * P, generator=g).to(dt)
+    w = 1 + 0.1 * torch.randn(P, generator=g)
+    zc, wc = z.cuda(), w.cuda()
+    ys, h = [], d["h0"]
+    for a, b in ((0, cut), (cut, L)):
+        y, h = axon_ssm.delta_scan(*(d[n][:, a:b].contiguous() for n in SEQ), params, h)
+        ys.append(axon_ssm.gated_norm(y.flatten(2), wc, zc[:, a:b].contiguous(), group=P))
+    for t in range(L, L + steps):
+        y = axon_ssm.delta_step(*(d[n][:, t].contiguous() for n in SEQ), params, h)
+        ys.append(axon_ssm.gated_norm(y.flatten(1), wc, zc[:, t], group=P)[:, None])
+    got = torch.cat(ys, 1).float().cpu().numpy()
+    y_ref, h_ref = ref(inp)
+    o_ref = oracle.gated_norm(y_ref.reshape(B, L + steps, H * P), P, "rms", "after", True, z, w)
+    # the norm sees y rounded to the io type, and rounds once more
+    close(got, o_ref, 1e-5 if io == "f32" else 2.6e-3 + 2.3e-3, "normed output", None if io == "f32" else 4e-2)
+    close(h.cpu().numpy(), h_ref, 1e-5, "state")

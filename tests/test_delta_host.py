@@ -1,0 +1,206 @@
+"""The gated delta rule and the grouped gated norm without a GPU: the fp64
+oracle against forms that share nothing with its loop, and the C ABI's and the
+binding's refusals (fake, never dereferenced pointers: every call fails
+argument validation, so nothing is launched)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+FAKE = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from selective_state_space_52_b200 import build
+    build.build()
+    from selective_state_space_52_b200 import axon_ssm
+    return axon_ssm._lib
+
+
+# ------------------------------------------------------------ oracle pins
+def rand_delta(rng, B=2, L=23, G=2, H=4, P=5, N=6):
+    return dict(q=rng.standard_normal((B, L, G, N)), k=rng.standard_normal((B, L, G, N)),
+                v=rng.standard_normal((B, L, H, P)), dt_raw=rng.standard_normal((B, L, H)),
+                b_raw=rng.standard_normal((B, L, H)), dt_bias=rng.standard_normal(H) - 3,
+                A_log=rng.standard_normal(H), h0=rng.standard_normal((B, H, P, N)))
+
+
+def test_delta_matches_matrix_products():
+    """S_t as explicit products with a (I - beta k^ k^^T): numpy matrices."""
+    rng = np.random.default_rng(1)
+    d = rand_delta(rng)
+    y, h = oracle.delta_scan(**d)
+    B, L, H, P = d["v"].shape
+    N = d["k"].shape[-1]
+    for b in range(B):
+        for hd in range(H):
+            S = d["h0"][b, hd]
+            for t in range(L):
+                k, q = d["k"][b, t, hd // 2], d["q"][b, t, hd // 2]
+                k, q = (u / np.linalg.norm(np.append(u, 1e-3)) for u in (k, q))
+                a = np.exp(-np.exp(d["A_log"][hd]) * np.log1p(np.exp(d["dt_raw"][b, t, hd] + d["dt_bias"][hd])))
+                beta = 0.5 * (1 + np.tanh(d["b_raw"][b, t, hd] / 2))
+                S = a * S @ (np.eye(N) - beta * np.outer(k, k)) + beta * np.outer(d["v"][b, t, hd], k)
+                np.testing.assert_allclose(y[b, t, hd], S @ q / np.sqrt(N), rtol=1e-11, atol=1e-12)
+            np.testing.assert_allclose(h[b, hd], S, rtol=1e-11, atol=1e-12)
+
+
+def test_delta_replaces_what_a_key_held():
+    """beta = 1, no decay, unit keys: reading a key returns the last value written to it."""
+    N = P = 4
+    k = np.eye(N)[[0, 1, 0, 2, 1]][None, :, None]
+    v = np.random.default_rng(2).standard_normal((1, 5, 1, P))
+    y, h = oracle.delta_scan(k, k, v, np.full((1, 5, 1), -800.0), np.full((1, 5, 1), 800.0), np.zeros(1), np.zeros(1),
+                             norm=False, scale=1.0)
+    np.testing.assert_allclose(y, v, atol=1e-14)
+    np.testing.assert_allclose(h[0, 0].T, np.stack([v[0, 2, 0], v[0, 4, 0], v[0, 3, 0], np.zeros(P)]), atol=1e-14)
+
+
+def test_delta_split_sequence_and_lengths():
+    d = rand_delta(np.random.default_rng(3), L=17)
+    y, h = oracle.delta_scan(**d)
+    cut = {n: t[:, :6] if t.ndim > 2 and n != "h0" else t for n, t in d.items()}
+    y1, h1 = oracle.delta_scan(**cut)
+    rest = {n: t[:, 6:] if t.ndim > 2 and n != "h0" else t for n, t in d.items()}
+    y2, h2 = oracle.delta_scan(**{**rest, "h0": h1})
+    np.testing.assert_array_equal(np.concatenate([y1, y2], 1), y)
+    np.testing.assert_array_equal(h2, h)
+    y3, h3 = oracle.delta_scan(**d, lengths=np.array([6, 0]))
+    np.testing.assert_array_equal(y3[0, :6], y1[0])
+    np.testing.assert_array_equal(h3, np.stack([h1[0], d["h0"][1]]))
+    assert not y3[0, 6:].any() and not y3[1].any()
+
+
+@pytest.mark.parametrize("kind", ["rms", "group"])
+@pytest.mark.parametrize("gate", [None, "after", "before"])
+def test_gated_norm_matches_torch(kind, gate):
+    g = torch.Generator().manual_seed(4)
+    x, z = (torch.randn(5, 24, generator=g, dtype=torch.float64) for _ in range(2))
+    w, b = (torch.randn(24, generator=g, dtype=torch.float64) for _ in range(2))
+    silu = torch.nn.functional.silu
+    t = x * silu(z) if gate == "before" else x
+    if kind == "group":
+        o = torch.nn.functional.group_norm(t, 3, w, b, 1e-5)
+    else:
+        o = torch.nn.functional.rms_norm(t.view(5, 3, 8), (8,), eps=1e-5).view(5, 24) * w + b
+    o = o * silu(z) if gate == "after" else silu(o) if gate is None else o
+    got = oracle.gated_norm(x, 8, kind, gate, True, z, w, b, 1e-5)
+    np.testing.assert_allclose(got, o.numpy(), rtol=1e-12, atol=1e-13)
+
+
+# ------------------------------------------------------------ refusals of the C ABI
+def scan(lib, **over):
+    a = dict(B=1, L=64, H=4, G=2, P=64, N=128, io=1, q=FAKE, ldq=256, k=FAKE + (1 << 24), ldk=256, v=FAKE + (2 << 24),
+             ldv=256, dt_raw=FAKE + (3 << 24), b_raw=FAKE + (4 << 24), dt_bias=FAKE + (5 << 24),
+             A_log=FAKE + (6 << 24), lengths=None, h0=None, scale=0.1, norm=1, y=FAKE + (7 << 24),
+             h_out=FAKE + (8 << 24), workspace=FAKE + (9 << 24), workspace_bytes=1 << 24, stream=None)
+    a.update(over)
+    return lib.axon_delta_scan_fwd(*a.values())
+
+
+@pytest.mark.parametrize("over, status", [
+    (dict(B=-1), 1), (dict(L=-1), 1), (dict(H=-1), 1),
+    (dict(H=5), 2), (dict(G=0), 2), (dict(P=32), 2), (dict(N=96), 2), (dict(io=2), 2), (dict(B=70000), 2),
+    (dict(L=1 << 30), 2),
+    (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(dt_raw=None), 1), (dict(b_raw=None), 1),
+    (dict(dt_bias=None), 1), (dict(A_log=None), 1), (dict(y=None), 1), (dict(h_out=None), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
+    (dict(ldq=248), 1), (dict(ldk=128), 1), (dict(ldv=255), 1),
+    (dict(ldq=260), 3), (dict(ldv=257), 3), (dict(q=FAKE + 8), 3), (dict(y=FAKE + (7 << 24) + 2), 3),
+    (dict(h0=FAKE + (10 << 24) + 4), 3), (dict(lengths=FAKE + (10 << 24) + 2), 3), (dict(io=0, ldq=258), 3),
+    (dict(y=FAKE), 1), (dict(y=FAKE + (2 << 24)), 1), (dict(h_out=FAKE + (1 << 24)), 1),
+    (dict(y=FAKE + (8 << 24)), 1), (dict(h0=FAKE + (8 << 24) + 64), 1), (dict(lengths=FAKE + (7 << 24)), 1),
+    (dict(h_out=FAKE + (6 << 24)), 1),
+])
+def test_delta_scan_rejects(lib, over, status):
+    assert scan(lib, **over) == status
+
+
+def test_delta_scan_rejects_strided_overlap(lib):
+    # 64 tokens 4096 elements apart reach 516096 bytes in: y in a gap between two tokens still lies inside
+    assert scan(lib, ldv=4096, y=FAKE + (2 << 24) + 4096 * 2 * 62 + 1024) == 1
+
+
+def test_delta_noop_sizes(lib):
+    assert scan(lib, B=0) == 0
+    assert scan(lib, H=0) == 0
+
+
+def step(lib, **over):
+    a = dict(B=2, H=4, G=2, P=64, N=128, io=1, q=FAKE, ldq=256, k=FAKE + (1 << 24), ldk=256, v=FAKE + (2 << 24),
+             ldv=256, dt_raw=FAKE + (3 << 24), b_raw=FAKE + (4 << 24), dt_bias=FAKE + (5 << 24),
+             A_log=FAKE + (6 << 24), scale=0.1, norm=1, state=FAKE + (7 << 24), y=FAKE + (8 << 24), stream=None)
+    a.update(over)
+    return lib.axon_delta_step(*a.values())
+
+
+@pytest.mark.parametrize("over, status", [
+    (dict(B=-1), 1), (dict(H=6, G=4), 2), (dict(P=48), 2), (dict(N=256), 2), (dict(io=7), 2), (dict(B=1 << 20), 2),
+    (dict(q=None), 1), (dict(state=None), 1), (dict(y=None), 1), (dict(ldk=16), 1), (dict(ldk=257), 3),
+    (dict(state=FAKE + (7 << 24) + 8), 3), (dict(y=FAKE), 1), (dict(state=FAKE + (2 << 24)), 1),
+    (dict(y=FAKE + (7 << 24) + 256), 1), (dict(scale=float("nan")), 1),
+])
+def test_delta_step_rejects(lib, over, status):
+    assert step(lib, **over) == status
+    assert step(lib, B=0) == 0
+
+
+def norm(lib, **over):
+    a = dict(rows=8, C=256, D=64, io=1, kind=0, gate=1, act=1, x=FAKE, ldx=256, z=FAKE + (1 << 24), ldz=256,
+             w=FAKE + (2 << 24), b=None, per_channel=0, eps=1e-6, y=FAKE + (3 << 24), ldy=256, stream=None)
+    a.update(over)
+    return lib.axon_gated_norm_fwd(*a.values())
+
+
+@pytest.mark.parametrize("over, status", [
+    (dict(rows=-1), 1), (dict(D=0), 1), (dict(D=-64), 1), (dict(D=96), 1), (dict(C=-256), 1), (dict(io=2), 2),
+    (dict(kind=2), 2), (dict(gate=3), 2), (dict(C=16384, D=16384, ldx=16384, ldy=16384, ldz=16384), 2),
+    (dict(rows=1 << 30, D=8), 2), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
+    (dict(x=None), 1), (dict(z=None), 1), (dict(y=None), 1), (dict(ldx=128), 1), (dict(ldz=248), 1), (dict(ldy=0), 1),
+    (dict(C=260, D=4, ldx=264, ldz=264, ldy=264), 3), (dict(ldx=260), 3), (dict(x=FAKE + 2), 3), (dict(w=FAKE + (2 << 24) + 4), 3),
+    (dict(y=FAKE + 512), 1), (dict(ldx=512, ldy=512, y=FAKE + 256), 1), (dict(ldx=512, ldy=512, y=FAKE + 768 + 4096), 1), (dict(y=FAKE, ldy=512), 1), (dict(y=FAKE + (1 << 24) + 1024), 1), (dict(y=FAKE + (2 << 24)), 1),
+])
+def test_gated_norm_rejects(lib, over, status):
+    assert norm(lib, **over) == status
+
+
+def test_gated_norm_noop_sizes(lib):
+    assert norm(lib, rows=0) == 0
+    assert norm(lib, C=0) == 0
+
+
+# ------------------------------------------------------------ refusals of the binding
+def test_binding_refuses_cpu_tensors(lib):
+    from selective_state_space_52_b200 import axon_ssm
+    t = torch.zeros(1, 4, 2, 64)
+    r = torch.zeros(1, 4, 2)
+    params = {"dt_bias": torch.zeros(2), "A_log": torch.zeros(2)}
+    with pytest.raises(ValueError, match="CUDA device"):
+        axon_ssm.delta_scan(t, t, t, r, r, params)
+    with pytest.raises(ValueError, match="CUDA device"):
+        axon_ssm.delta_step(t[:, 0], t[:, 0], t[:, 0], r[:, 0], r[:, 0], params, torch.zeros(1, 2, 64, 64))
+    with pytest.raises(ValueError, match="CUDA device"):
+        axon_ssm.gated_norm(torch.zeros(4, 64))
+
+
+def test_binding_token_strides(lib):
+    from selective_state_space_52_b200.axon_ssm import _row_stride, _token_stride
+    row = torch.zeros(2, 5, 10 * 64)
+    q, k, v = row[..., :128].view(2, 5, 2, 64), row[..., 128:256].view(2, 5, 2, 64), row[..., 256:].view(2, 5, 6, 64)
+    assert [_token_stride("f", "t", t) for t in (q, k, v)] == [640] * 3
+    assert _token_stride("f", "t", v[:, :1]) == 3200                # one token a row: the rows' own stride
+    assert _token_stride("f", "t", v[:1, :1]) == 6 * 64             # one token in all: any stride will do
+    assert _token_stride("f", "t", q[:, 0]) == 3200
+    for bad in (q[:, ::1, :, ::2], row.view(2, 5, 10, 64)[:, :, ::2], row.view(2, 5, 10, 64)[:, :4], q.transpose(0, 1)):
+        with pytest.raises(ValueError):
+            _token_stride("f", "t", bad)
+    assert _row_stride("f", "t", row[..., :128], 10, 128) == 640
+    assert _row_stride("f", "t", row[0, :, 128:], 5, 512) == 640
+    with pytest.raises(ValueError):
+        _row_stride("f", "t", row[:, :4, :128], 8, 128)
+    with pytest.raises(ValueError):
+        _row_stride("f", "t", row[..., ::2], 10, 320)
