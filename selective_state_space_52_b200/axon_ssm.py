@@ -675,6 +675,13 @@ def _delta_args(what, q, k, v, dt_raw, b_raw, params, scale):
         (N ** -0.5 if scale is None else float(scale))
 
 
+def delta_error_flag(workspace) -> int:
+    """The delta rule's error flag (the workspace's first int) after the call
+    that used ``workspace`` has completed.  Synchronises the device."""
+    torch.cuda.synchronize(workspace.device)
+    return int(workspace[:4].view(torch.int32).item())
+
+
 def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, scale=None, qk_norm=True, out=None,
                workspace=None, stream=None, check=True):
     """Gated delta rule prefill: q, k (B,L,G,N), v (B,L,H,P), dt_raw, b_raw
@@ -708,15 +715,16 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     state = (Bsz, H, P, N)
     _like("delta_scan", torch.float32, h0=(h0, state), h_out=(h_out, state), y=(y, v.shape, v.dtype),
           lengths=(lengths, (Bsz,), torch.int32))
-    if workspace is None:
-        nbytes = axon_delta_workspace_bytes(Bsz, L, H, G, P, N, io)
-        if nbytes > 0:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            made.append(workspace)
+    nbytes = axon_delta_workspace_bytes(Bsz, L, H, G, P, N, io)
+    if workspace is None and nbytes > 0:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        made.append(workspace)
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
     axon_delta_scan_fwd(Bsz, L, H, G, P, N, io, *args, lengths, h0, scale, int(qk_norm), y, h_out, workspace, wsz,
                         stream=stream)
     _used_on(stream, dev, *made)
+    if check and nbytes > 0 and delta_error_flag(workspace) != 0:
+        raise AxonError(6, "axon_delta_scan_fwd (a wait for a copy or a tensor-core product gave up)")
     return y, h_out
 
 

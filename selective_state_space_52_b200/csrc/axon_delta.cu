@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "axon_ssm.h"
+#include "delta.cuh"
 #include "delta_step.cuh"
 #include "gated_norm.cuh"
 
@@ -89,6 +90,58 @@ void launch_recur(const DeltaParams& p, cudaStream_t st) {
         delta_recur_kernel<Io, N, 1><<<dim3((unsigned)(p.P / ROWS1), (unsigned)p.H, (unsigned)p.B), 128, 0, st>>>(p);
 }
 
+// bf16 sequences of at least this many tokens go in chunks.
+constexpr int kChunkedFrom = 32;
+bool chunked(int L, axon_dtype io) { return io == AXON_BF16 && L >= kChunkedFrom; }
+
+struct DeltaWs {
+    size_t err, kq, blob, total;
+};
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+DeltaWs delta_ws(int B, int L, int H, int G, int N) {
+    const size_t nC = ((size_t)L + kDlC - 1) / kDlC;
+    DeltaWs w{};
+    w.err = 0;
+    w.kq = 256;
+    w.blob = w.kq + (size_t)B * G * nC * 128 * N * 2;
+    w.total = w.blob + up256((size_t)B * H * nC * kDlBlob);
+    return w;
+}
+
+// Raises a kernel's dynamic shared memory limit, once per device.
+template <class K>
+bool allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+    const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (bit) done.fetch_or(bit, std::memory_order_acq_rel);
+    return true;
+}
+
+template <int N, int P>
+axon_status launch_chunked(const DeltaChunkParams& p, cudaStream_t st) {
+    static std::atomic<unsigned long long> prep_ok{0}, walk_ok{0};
+    if (!allow_smem(delta_prep_kernel<N>, DeltaPrepSmem<N>::TOTAL, prep_ok) ||
+        !allow_smem(delta_walk_kernel<N, P>, DeltaWalkSmem<N, P>::TOTAL, walk_ok))
+        return AXON_ERR_CUDA;
+    delta_prep_kernel<N><<<dim3((unsigned)p.nC, (unsigned)p.d.G, (unsigned)p.d.B), 128, DeltaPrepSmem<N>::TOTAL, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return AXON_ERR_CUDA;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)p.d.H, (unsigned)p.d.B, 1);
+    c.blockDim = dim3(kDlThreads, 1, 1);
+    c.dynamicSmemBytes = DeltaWalkSmem<N, P>::TOTAL;
+    c.stream = st;
+    c.attrs = pdl;
+    c.numAttrs = 1;
+    if (cudaLaunchKernelEx(&c, delta_walk_kernel<N, P>, p) != cudaSuccess) return AXON_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? AXON_OK : AXON_ERR_CUDA;
+}
+
 // Lanes a group and pieces a lane: the fewest lanes (4 .. 32) that hold the
 // group in one piece each, then more pieces, then whole blocks.
 template <class Io>
@@ -117,8 +170,8 @@ using namespace axon;
 extern "C" {
 
 size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io) {
-    (void)B; (void)L; (void)H; (void)G; (void)P; (void)N; (void)io;
-    return 0;
+    if (B <= 0 || L < 0 || H <= 0 || !shape_ok(H, G, P, N) || !chunked(L, io)) return 0;
+    return delta_ws(B, L, H, G, N).total;
 }
 
 axon_status axon_delta_scan_fwd(int B, int L, int H, int G, int P, int N, axon_dtype io,
@@ -154,6 +207,13 @@ axon_status axon_delta_scan_fwd(int B, int L, int H, int G, int P, int N, axon_d
 
     DeltaParams p{B, L, H, G, P, ldq, ldk, ldv, q, k, v, dt_raw, b_raw, dt_bias, A_log, lengths, h0, y, h_out, scale, qk_norm != 0};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (chunked(L, io)) {
+        const DeltaWs w = delta_ws(B, L, H, G, N);
+        unsigned char* ws = static_cast<unsigned char*>(workspace);
+        const DeltaChunkParams c{p, (L + kDlC - 1) / kDlC, ws + w.kq, ws + w.blob, reinterpret_cast<int*>(ws + w.err)};
+        if (N == 128) return P == 128 ? launch_chunked<128, 128>(c, st) : launch_chunked<128, 64>(c, st);
+        return P == 128 ? launch_chunked<64, 128>(c, st) : launch_chunked<64, 64>(c, st);
+    }
     if (io == AXON_BF16) N == 128 ? launch_recur<IoBF16, 128>(p, st) : launch_recur<IoBF16, 64>(p, st);
     else N == 128 ? launch_recur<IoF32, 128>(p, st) : launch_recur<IoF32, 64>(p, st);
     return cudaGetLastError() == cudaSuccess ? AXON_OK : AXON_ERR_CUDA;
