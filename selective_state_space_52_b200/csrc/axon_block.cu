@@ -10,7 +10,6 @@
 // below): one launch writes x and z, one writes dt_raw, B and C, one the
 // output; the conv stage and the scan are this library's kernels too.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -22,6 +21,7 @@
 #include "device_math.cuh"
 #include "gemm_pair.cuh"
 #include "gemm_tc.cuh"
+#include "tensor_map.cuh"
 
 namespace axon {
 namespace {
@@ -72,20 +72,6 @@ bool plan_block(int B, int L, int E, int N, int K, BlockPlan* p) {
     p->scan_ws = off; off += round_up(p->scan_ws_bytes);
     p->total = off;
     return true;
-}
-
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
 }
 
 // A 2-D bf16 tensor map over a row-major (rows x cols, row stride ld

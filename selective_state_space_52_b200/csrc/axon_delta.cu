@@ -12,6 +12,7 @@
 #include "delta.cuh"
 #include "delta_step.cuh"
 #include "gated_norm.cuh"
+#include "tensor_map.cuh"
 
 namespace axon {
 namespace {
@@ -120,12 +121,27 @@ bool allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& done) {
     return true;
 }
 
+// V as (channels, tokens, batch rows): boxes of one head's 64 tokens, tokens
+// past the end read as zeros.
+bool v_map(CUtensorMap* m, const DeltaParams& d) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d.H * d.P, (cuuint64_t)d.L, (cuuint64_t)d.B};
+    const cuuint64_t strides[2] = {(cuuint64_t)d.ldv * 2, (cuuint64_t)d.L * d.ldv * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)d.P, kDlC, 1}, estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(d.v), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int N, int P>
 axon_status launch_chunked(const DeltaChunkParams& p, cudaStream_t st) {
     static std::atomic<unsigned long long> prep_ok{0}, walk_ok{0};
     if (!allow_smem(delta_prep_kernel<N>, DeltaPrepSmem<N>::TOTAL, prep_ok) ||
         !allow_smem(delta_walk_kernel<N, P>, DeltaWalkSmem<N, P>::TOTAL, walk_ok))
         return AXON_ERR_CUDA;
+    CUtensorMap tmV;
+    if (!v_map(&tmV, p.d)) return AXON_ERR_CUDA;
     delta_prep_kernel<N><<<dim3((unsigned)p.nC, (unsigned)p.d.G, (unsigned)p.d.B), 128, DeltaPrepSmem<N>::TOTAL, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return AXON_ERR_CUDA;
     cudaLaunchAttribute pdl[1];
@@ -138,7 +154,7 @@ axon_status launch_chunked(const DeltaChunkParams& p, cudaStream_t st) {
     c.stream = st;
     c.attrs = pdl;
     c.numAttrs = 1;
-    if (cudaLaunchKernelEx(&c, delta_walk_kernel<N, P>, p) != cudaSuccess) return AXON_ERR_CUDA;
+    if (cudaLaunchKernelEx(&c, delta_walk_kernel<N, P>, tmV, p) != cudaSuccess) return AXON_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? AXON_OK : AXON_ERR_CUDA;
 }
 

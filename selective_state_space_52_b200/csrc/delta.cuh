@@ -21,21 +21,27 @@
 // in lane v and belong to one thread, which holds the float32 state row in
 // registers.  No value ever crosses a lane; the A operands are what the thread
 // itself writes to its lane, and the B operands are the tiles K, Q, T, M as
-// they lie in shared memory.
+// they lie in shared memory.  T and M are triangular, so their products go in
+// two halves of 32 tokens without the zero block, and each half starts when
+// its part of R is there: the conversions of one half run beside the products
+// of the other.
 //
 // Precision.  Operands are fp16 with float32 accumulators.  K and Q enter
 // scaled by a power of two per token (largest element in [1/2, 1)): exact, but
 // for bits below 2^-25 of the row.  S, R, U (for the state) and T enter as two
-// fp16 parts, hi + lo, 22 significant bits; the lo x lo term is dropped.  fp16
+// fp16 parts, hi + lo, 21 significant bits; the lo x lo term is dropped.  fp16
 // needs values near 1, so each lane carries a power-of-two scale lambda_v: all
-// of the walk is linear in lane v, so S, R, U and Y simply live in units of
-// 1 / lambda_v; a lane rescales when its largest value leaves [2^-3, 2^6].
-// Two bf16 parts (no scale needed) measured 4.5e-6 on the final state in a
-// float64 model of these roundings, fp16 parts about 1e-7: the state is a
-// float32 output, and the product count is the same.  Y takes one fp16 part of
-// S, U and M (2^-12 each, below its bf16 rounding).
+// of the walk is linear in lane v, so S, V, R, U and Y simply live in units of
+// 1 / lambda_v.  Before each chunk a lane whose largest of |S| and |V| has left
+// [2^-3, 2^6] rescales; with keys of length at most 1 no product of the chunk
+// then exceeds 64 (1 + 64) + 64 sqrt(N) < 2^13, far inside fp16.
+// Two bf16 parts (no scale needed) came to 4.5e-6 on the final state in a
+// float64 model of these roundings, and three to half again as many products;
+// measured with fp16 parts: 5e-7.  Y takes one fp16 part of S, U and M (2^-11
+// each, below its bf16 rounding).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "delta_step.cuh"
@@ -46,13 +52,13 @@ namespace axon {
 
 constexpr int kDlC = 64;                       // tokens per chunk
 constexpr int kDlTile = kDlC * kDlC * 2;       // a 64 x 64 fp16 tile: 8 KB
-constexpr int kDlVec = 4 * kDlC * 4;           // ek, eG, wk, oq
+constexpr int kDlVec = 4 * kDlC * 4;           // four rows: -ek, eq, wk, (el, y scale)
 constexpr int kDlBlob = 3 * kDlTile + kDlVec;  // per chunk and value head: T hi, T lo, M, vectors
 
 struct DeltaChunkParams {
     DeltaParams d;
     int nC;                      // chunks of L
-    unsigned char* kq;           // (B, G, nC): [K'; Q'] fp16, 128 rows in 64-column blocks, 128-byte swizzle
+    unsigned char* kq;           // (B, G, nC): K', then Q': fp16, 64 rows in 64-column blocks, 128-byte swizzle
     unsigned char* blob;         // (B, H, nC): kDlBlob bytes
     int* err;                    // set to 1 when a wait gave up
 };
@@ -67,21 +73,22 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// x - (the fp16 in the low / high half of h), float32
-__device__ __forceinline__ float f16_rest_lo(uint32_t h, float x) {
-    float d;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tsub.f32.f16 %0, a, %2;\n\t}" : "=f"(d) : "r"(h), "f"(x));
-    return -d;
+// A pair as hi + lo fp16 parts: hi the leading 11 bits (cut off, so that the
+// rest is one exact subtraction), lo the rest rounded.  Five instructions a
+// pair; with hi rounded instead, converting it back to subtract it took half
+// as long again.
+__device__ __forceinline__ void split_f16(float2 x, uint32_t& hi, uint32_t& lo) {
+    const float2 h = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffffe000u),
+                                 __uint_as_float(__float_as_uint(x.y) & 0xffffe000u));
+    const float2 r = __ffma2_rn(h, make_float2(-1.0f, -1.0f), x);
+    hi = pack_f16(h.x, h.y);
+    lo = pack_f16(r.x, r.y);
 }
-__device__ __forceinline__ float f16_rest_hi(uint32_t h, float x) {
+// a b + c with a and b in bf16
+__device__ __forceinline__ float fma_bf16(unsigned short a, unsigned short b, float c) {
     float d;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tsub.f32.f16 %0, b, %2;\n\t}" : "=f"(d) : "r"(h), "f"(x));
-    return -d;
-}
-// a pair as hi + lo fp16 parts
-__device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_f16(a, b);
-    lo = pack_f16(f16_rest_lo(hi, a), f16_rest_hi(hi, b));
+    asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(a), "h"(b), "f"(c));
+    return d;
 }
 // max(m, |a|, |b|)
 __device__ __forceinline__ float max_abs3(float m, float a, float b) {
@@ -111,16 +118,17 @@ struct DeltaPrepSmem {
     static constexpr int A = 0;                          // ... then A (float32), later the T parts over it
     static constexpr int M = kDlC * LDA * 4;             // M tile
     static constexpr int KQ_BYTES = 128 * N * 2;
-    static constexpr int V = KQ_BYTES > M + kDlTile ? KQ_BYTES : M + kDlTile;   // vectors ek, eG, wk, oq
+    static constexpr int V = KQ_BYTES > M + kDlTile ? KQ_BYTES : M + kDlTile;   // the vectors
     static constexpr int RK = V + kDlVec;                // rk'
-    static constexpr int RQ = RK + kDlC * 4;             // scale rq'
+    static constexpr int RQ = RK + kDlC * 4;             // rq', the largest in [1/2, 1)
     static constexpr int GH = RQ + kDlC * 4;             // Gamma (log2 units), float hi and lo parts
     static constexpr int GL = GH + kDlC * 4;
     static constexpr int BE = GL + kDlC * 4;             // beta
     static constexpr int TOT = BE + kDlC * 4;            // double: the first warp's total
     static constexpr int MB = TOT + 8;
     static constexpr int SLOT = MB + 8;
-    static constexpr int BYTES = SLOT + 8;
+    static constexpr int YS = SLOT + 4;                  // scale times what RQ was divided by
+    static constexpr int BYTES = YS + 4;
     static constexpr int TOTAL = BYTES + 1024;           // with the alignment pad
     static_assert(2 * kDlTile <= M, "the T parts fit over A");
     static_assert(M % 16 == 0 && V % 16 == 0 && TOT % 8 == 0, "alignment");
@@ -231,10 +239,10 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
                     h[q] = pack_f16(x0, x1);
                 }
                 const int pc = l + 8 * i;
-                const int off = (pc >> 3) * 16384 + r * 128 + (((pc & 7) ^ (r & 7)) << 4);
+                const int in_row = ((pc & 7) ^ (r & 7)) << 4;
                 const uint4 o = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(sm + Lay::KQ + off) = o;
-                *reinterpret_cast<uint4*>(out + off) = o;
+                *reinterpret_cast<uint4*>(sm + Lay::KQ + (pc >> 3) * 16384 + r * 128 + in_row) = o;
+                *reinterpret_cast<uint4*>(out + (r >> 6) * (Lay::KQ_BYTES / 2) + (pc >> 3) * 8192 + (r & 63) * 128 + in_row) = o;
             }
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -243,7 +251,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
                 const float es = pow2i(e);
                 const float f1 = d.norm ? es * rsqrtf(fmaf(ss * es, es, kDeltaEps)) : es;
                 if (r < C) rk[r] = f1;
-                else rq[r - C] = d.scale * f1;
+                else rq[r - C] = f1;
             }
         }
     }
@@ -259,6 +267,15 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
             umma(tbase, dsc, dsc, umma_idesc_f16(128, C, 0, 0), ks > 0);      // [K'; Q'] K'^T
         }
         umma_commit(sb + Lay::MB);
+    }
+    if (w == 3) {                                        // rq' to [1/2, 1), the rest of it to the outputs' scale
+        float m = fmaxf(rq[lane], rq[lane + 32]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int e = exp_above(m);
+        rq[lane] *= pow2i(-e);
+        rq[lane + 32] *= pow2i(-e);
+        if (lane == 0) *reinterpret_cast<float*>(sm + Lay::YS) = d.scale * pow2i(e);
     }
     const bool ok = mbar_wait(sb + Lay::MB, 0u);
     const bool failed = __syncthreads_or(!ok);           // KQ is free from here on: A and M lie over it
@@ -308,13 +325,14 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
         const float ghi = gh[i], glo = gl[i];
         if (w < 2) {
             const float eg = ex2_approx(ghi);
-            vec[i] = eg * rk[i];
-            vec[C + i] = eg;
+            vec[i] = -eg * rk[i];
+            vec[C + i] = eg * rq[i];
             vec[2 * C + i] = ex2_approx((gh[C - 1] - ghi) + (gl[C - 1] - glo)) * rk[i];
-            vec[3 * C + i] = rq[i];
+            if (i == C - 1) vec[3 * C] = eg;
+            if (i == 0) vec[3 * C + 1] = *reinterpret_cast<const float*>(sm + Lay::YS);
         }
         // ---- row i of A, or of M
-        const float f = w < 2 ? be[i] * rk[i] : 1.f;
+        const float f = w < 2 ? be[i] * rk[i] : rq[i];
         const int edge = w < 2 ? i : i + 1;              // columns below it belong to the triangle
 #pragma unroll
         for (int j0 = 0; j0 < C; j0 += 16) {
@@ -356,7 +374,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
 #pragma unroll
             for (int q = 0; q < C / 2; ++q) {            // rows 2q, 2q + 1: neighbouring lanes trade halves
                 uint32_t hi, lo;
-                split_f16(t[q].x * bj, t[q].y * bj, hi, lo);
+                split_f16(make_float2(t[q].x * bj, t[q].y * bj), hi, lo);
                 const uint32_t oh = __shfl_xor_sync(0xffffffffu, hi, 1), ol = __shfl_xor_sync(0xffffffffu, lo, 1);
                 const int row = 2 * q + odd;
                 const int off = row * 128 + ((((tid & ~1) >> 3) ^ (row & 7)) << 4) + (tid & 6) * 2;
@@ -383,33 +401,50 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
     if (w == 0 && !failed) tmem_dealloc(tbase, 64);      // after a failed wait a late product might still write
 }
 
-// ---- the walk: grid = (H, B), 160 threads; warps 0 .. P/32 - 1 compute (thread =
-// tensor-memory lane = value column), warp 4 copies tiles in and issues products
-constexpr int kDlThreads = 160;
+// ---- the walk: grid = (H, B), 576 threads.  Warps 0 .. 15 compute: warp w holds
+// lanes 32 (w & 3) .. of tensor memory, and the four warps of such a quadrant
+// share its lanes' work, thread `part` = w >> 2 of a lane taking a quarter of
+// the state row and of the tokens.  (One warp a quadrant, two blocks an SM,
+// took 12 thousand cycles a chunk: with one warp a scheduler nothing hides the
+// latencies of the conversions.)  Warp 16 copies tiles in and issues products,
+// warp 17 finds the columns' largest |v| a chunk ahead.
+constexpr int kDlThreads = 576;
+constexpr int kDlStages = 3;
 
 template <int N, int P>
 struct DeltaWalkSmem {
-    static constexpr int KQ_BYTES = 128 * N * 2;
-    static constexpr int KQ = 0;                          // two stages
-    static constexpr int T = KQ + 2 * KQ_BYTES;           // T hi, T lo
+    static constexpr int K_BYTES = kDlC * N * 2;
+    static constexpr int V_BYTES = kDlC * P * 2;
+    // a stage: all of a chunk's tiles
+    static constexpr int K = 0;
+    static constexpr int Q = K + K_BYTES;
+    static constexpr int T = Q + K_BYTES;                 // T hi, T lo
     static constexpr int M = T + 2 * kDlTile;
-    static constexpr int V = M + kDlTile;                 // 64 rows of P bf16
-    static constexpr int VEC = V + kDlC * P * 2;          // two stages
-    static constexpr int MB = VEC + 2 * kDlVec;
-    enum { FULL_KQ0, FULL_KQ1, FULL_V, FULL_T, FULL_M, X_K, X_Q, UR, YM, D_A, D_B, S_IN, R_IN, U_IN, Y_OUT, DRAIN, BARS };
+    static constexpr int VEC = M + kDlTile;
+    static constexpr int V = VEC + kDlVec;                // 64 rows of P bf16
+    static constexpr int STAGE = V + V_BYTES;
+    static constexpr int VM = kDlStages * STAGE;          // largest |v| of the columns, per stage
+    static constexpr int SMAX = VM + kDlStages * P * 4;   // largest |S| of the quarters of a lane's state row
+    static constexpr int MB = SMAX + 4 * 128 * 4;
+    enum { FULL, VMAX = FULL + kDlStages, X_K0 = VMAX + kDlStages, X_K1, X_Q, U_0, U_1, Y_M, D, S_IN, R_IN0, R_IN1, U_IN0,
+           U_IN1, Y_OUT, QUAD, DRAIN = QUAD + 4, BARS };
     static constexpr int DEAD = MB + 8 * BARS;            // a wait gave up
     static constexpr int SLOT = DEAD + 4;
     static constexpr int BYTES = SLOT + 4;
     static constexpr int TOTAL = BYTES + 1024;
-    // tensor memory (256 columns): S hi 0 .. 63, S lo 64 .. 127, K S^T 128 .. 191, Q S^T 192 .. 255;
-    // then R hi 64 .. 95, lo 96 .. 127; U 0 .. 63; U_w hi and lo over R, U hi 160 .. 191; Y over Q S^T;
-    // the state's increment 0 .. 63 and (n >= 64) 128 .. 191
-    static constexpr int COLS = 256;
+    static_assert(TOTAL <= 227 * 1024, "shared memory of a block");
+    static_assert(STAGE % 1024 == 0 && VEC % 128 == 0, "swizzled tiles and copies aligned");
+    // tensor memory: the A operands hold two fp16 a column; 16 tokens of R and U_w are 8 columns hi, 8 lo
+    static constexpr int S_HI = 0, S_LO = 64, DD = 0;     // the state's increment comes where S was
+    static constexpr int XK = 128, XQ = 192;              // K S^T; Q S^T, scaled, then Y
+    static constexpr int R = 256, U = 320, UW = 384, UH = 448;
+    static constexpr int COLS = 512;
 };
 
-// The warp polls an mbarrier's phase; gives up after a bounded number of
+// The warp waits for an mbarrier's phase; gives up after a bounded number of
 // polls, or when another warp of the block has.  The same answer in every lane.
 __device__ __forceinline__ bool delta_wait(uint32_t mbar, int use, volatile int* dead) {
+    if (__all_sync(0xffffffffu, mbar_wait(mbar, (uint32_t)(use & 1), 1))) return true;
     bool ok = false;
     for (int k = 0; k < 4096 && !ok; ++k) {
         ok = mbar_wait(mbar, (uint32_t)(use & 1), kTcWaitLimit / 4096);
@@ -419,11 +454,23 @@ __device__ __forceinline__ bool delta_wait(uint32_t mbar, int use, volatile int*
     if (!ok) *dead = 1;
     return ok;
 }
+// 8 consecutive columns of this thread's tensor-memory lane; 4 into it
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(r[q]);
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
+}
 
 template <int N, int P>
-__global__ void __launch_bounds__(kDlThreads, 2) delta_walk_kernel(DeltaChunkParams p) {
+__global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_constant__ CUtensorMap tmV, DeltaChunkParams p) {
     using Lay = DeltaWalkSmem<N, P>;
-    constexpr int C = kDlC, WARPS = P / 32, KS = N / 16;
+    constexpr int C = kDlC, KS = N / 16, ST = kDlStages;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
     const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
@@ -441,341 +488,333 @@ __global__ void __launch_bounds__(kDlThreads, 2) delta_walk_kernel(DeltaChunkPar
 
     if (tid == 0) {
         for (int i = 0; i < Lay::BARS; ++i)
-            mbar_init(bar(i), i >= Lay::S_IN && i <= Lay::Y_OUT ? WARPS : 1);
+            mbar_init(bar(i), i >= Lay::S_IN && i <= Lay::Y_OUT ? P / 8 : i >= Lay::QUAD && i < Lay::DRAIN ? 4 : 1);   // warps
         *dead = 0;
         fence_mbar_init();
     }
     grid_dep_wait();                                      // the prep kernel's tiles are written
     fence_proxy_async();
     // only now, or these columns might keep a prep block waiting that this one waits for
-    if (w == 4) tmem_alloc(sb + Lay::SLOT, Lay::COLS);
+    if (w == 16) tmem_alloc(sb + Lay::SLOT, Lay::COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(sm + Lay::SLOT);
 
-    if (w == 4) {
+    if (w == 16) {
         // ---------------- copies and products
-        const unsigned char* kq = p.kq + ((size_t)b * d.G + g) * p.nC * Lay::KQ_BYTES;
+        const unsigned char* kq = p.kq + ((size_t)b * d.G + g) * p.nC * (2 * Lay::K_BYTES);
         const unsigned char* blob = p.blob + ((size_t)b * d.H + h) * p.nC * kDlBlob;
-        const __nv_bfloat16* vg = static_cast<const __nv_bfloat16*>(d.v) + (size_t)b * d.L * d.ldv + (size_t)h * P;
-        auto load_kq = [&](int c) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(Lay::FULL_KQ0 + (c & 1)), Lay::KQ_BYTES);
-                bulk_load(sb + Lay::KQ + (c & 1) * Lay::KQ_BYTES, kq + (size_t)c * Lay::KQ_BYTES, Lay::KQ_BYTES,
-                          bar(Lay::FULL_KQ0 + (c & 1)));
+        auto load_chunk = [&](int c, int st) {            // V's rows past L read as zeros
+            if (elect_one()) {
+                const uint32_t full = bar(Lay::FULL + st), dst = sb + st * Lay::STAGE;
+                mbar_arrive_expect_tx(full, Lay::STAGE);
+                bulk_load(dst + Lay::K, kq + (size_t)c * 2 * Lay::K_BYTES, 2 * Lay::K_BYTES, full);
+                tma_load_3d(dst + Lay::V, &tmV, h * P, c * C, b, full);
+                bulk_load(dst + Lay::T, blob + (size_t)c * kDlBlob, kDlBlob, full);
             }
         };
-        auto load_v = [&](int c) {                        // the rows that exist, and the vectors
-            const int rows = min(C, len - c * C);
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(Lay::FULL_V), rows * P * 2 + kDlVec);
-                bulk_load(sb + Lay::VEC + (c & 1) * kDlVec, blob + (size_t)c * kDlBlob + 3 * kDlTile, kDlVec, bar(Lay::FULL_V));
-            }
-            __syncwarp();
-            for (int r = lane; r < rows; r += 32)
-                bulk_load(sb + Lay::V + r * P * 2, vg + (size_t)(c * C + r) * d.ldv, P * 2, bar(Lay::FULL_V));
-        };
-        auto load_t = [&](int c) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(Lay::FULL_T), 2 * kDlTile);
-                bulk_load(sb + Lay::T, blob + (size_t)c * kDlBlob, 2 * kDlTile, bar(Lay::FULL_T));
-            }
-        };
-        auto load_m = [&](int c) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(Lay::FULL_M), kDlTile);
-                bulk_load(sb + Lay::M, blob + (size_t)c * kDlBlob + 2 * kDlTile, kDlTile, bar(Lay::FULL_M));
-            }
-        };
-        int n_kq = 0, n_v = 0, n_t = 0, n_m = 0;          // copies issued
-        if (nC > 0) {
-            load_kq(0); load_v(0); load_t(0); load_m(0);
-            n_kq = n_v = n_t = n_m = 1;
-        }
-        constexpr uint32_t kIdN = umma_idesc_f16(128, C, 0, 0);      // B K-major: K', Q', T, M rows
-        constexpr uint32_t kIdS = umma_idesc_f16(128, 64, 0, 1);     // B: K' rows as the K dimension (MN-major)
+        static_assert(Lay::V - Lay::T == kDlBlob, "T, M and the vectors lie as in the blob");
+        int loaded = 0;
+        for (; loaded < min(nC, ST); ++loaded) load_chunk(loaded, loaded);
+        constexpr uint32_t kId64 = umma_idesc_f16(128, 64, 0, 0);    // B K-major: K', Q', T, M rows
+        constexpr uint32_t kId32 = umma_idesc_f16(128, 32, 0, 0);
+        constexpr uint32_t kIdS = umma_idesc_f16(128, N, 0, 1);      // B: K' rows as the K dimension (MN-major)
+        auto rows_desc = [&](uint32_t t, int ks) { return umma_desc(t + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024); };
         bool ok = true;
-        for (int c = 0; c < nC && ok; ++c) {
-            const uint32_t kt = sb + Lay::KQ + (c & 1) * Lay::KQ_BYTES, qt = kt + 8192;
-            auto kdesc = [&](uint32_t t, int ks) { return umma_desc(t + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024); };
-            ok = delta_wait(bar(Lay::FULL_KQ0 + (c & 1)), c >> 1, dead) && delta_wait(bar(Lay::S_IN), c, dead);
-            if (!ok) break;
+        for (int c = 0, st = 0, use = 0; c < nC; ++c) {
+            const uint32_t sg = sb + st * Lay::STAGE, kt = sg + Lay::K, qt = sg + Lay::Q;
+            if (!(ok = delta_wait(bar(Lay::FULL + st), use, dead) && delta_wait(bar(Lay::S_IN), c, dead))) break;
             tc_fence_after();
-            if (lane == 0) {                              // K S^T, both parts of S
+            if (elect_one()) {                            // K S^T, both parts of S, 32 tokens at a time
 #pragma unroll
-                for (int ks = 0; ks < 2 * KS; ++ks)
-                    umma_ts(tbase + 128, tbase + (ks / KS) * 64 + 8 * (ks % KS), kdesc(kt, ks % KS), kIdN, ks > 0);
-                umma_commit(bar(Lay::X_K));
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int ks = 0; ks < 2 * KS; ++ks)
+                        umma_ts(tbase + Lay::XK + 32 * half, tbase + (ks / KS) * Lay::S_LO + 8 * (ks % KS),
+                                rows_desc(kt + 4096 * half, ks % KS), kId32, ks > 0);
+                    umma_commit(bar(Lay::X_K0 + half));
+                }
             }
-            // the stage's last reader, the state product of chunk c - 1, is done (its increment has been read)
-            if (c + 1 < nC) { load_kq(c + 1); ++n_kq; }
-            if (c > 0 && !(ok = delta_wait(bar(Lay::Y_OUT), c - 1, dead))) break;
+            if (!(ok = c == 0 || delta_wait(bar(Lay::Y_OUT), c - 1, dead))) break;
             tc_fence_after();
-            if (lane == 0) {                              // Q S^T, the hi part
+            // chunk c - 1 is done with its stage: its increment and its Y have been read
+            if (c > 0 && loaded < nC) {
+                load_chunk(loaded, st == 0 ? ST - 1 : st - 1);
+                ++loaded;
+            }
+            if (elect_one()) {                            // Q S^T, the hi part
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) umma_ts(tbase + 192, tbase + 8 * ks, kdesc(qt, ks), kIdN, ks > 0);
+                for (int ks = 0; ks < KS; ++ks) umma_ts(tbase + Lay::XQ, tbase + Lay::S_HI + 8 * ks, rows_desc(qt, ks), kId64, ks > 0);
                 umma_commit(bar(Lay::X_Q));
             }
-            // U goes where S hi is: Q S^T has to be done with it
-            if (!(ok = delta_wait(bar(Lay::FULL_T), c, dead) && delta_wait(bar(Lay::R_IN), c, dead) &&
-                       delta_wait(bar(Lay::X_Q), c, dead))) break;
+            if (!(ok = delta_wait(bar(Lay::R_IN0), c, dead))) break;
             tc_fence_after();
-            if (lane == 0) {                              // U = T R: hi hi, lo hi (R lo), hi lo (T lo)
+            if (elect_one()) {                            // U = T R, R's first half: hi hi, lo hi (R lo), hi lo (T lo)
 #pragma unroll
-                for (int ks = 0; ks < 12; ++ks) {
-                    const int q = ks & 3, part = ks >> 2;
-                    umma_ts(tbase, tbase + 64 + (part == 1 ? 32 : 0) + 8 * q,
-                            umma_desc(sb + Lay::T + (part == 2 ? kDlTile : 0) + q * 32, 16, 1024), kIdN, ks > 0);
+                for (int ks = 0; ks < 6; ++ks) {
+                    const int q = ks & 1, part = ks >> 1;
+                    umma_ts(tbase + Lay::U, tbase + Lay::R + (part == 1 ? 8 : 0) + 16 * q,
+                            umma_desc(sg + Lay::T + (part == 2 ? kDlTile : 0) + q * 32, 16, 1024), kId64, ks > 0);
                 }
-                umma_commit(bar(Lay::UR));
+                umma_commit(bar(Lay::U_0));
             }
-            if (c + 1 < nC) { load_v(c + 1); ++n_v; }     // V was read before R came in
-            if (!(ok = delta_wait(bar(Lay::FULL_M), c, dead) && delta_wait(bar(Lay::U_IN), c, dead))) break;
+            if (!(ok = delta_wait(bar(Lay::R_IN1), c, dead))) break;
             tc_fence_after();
-            if (c + 1 < nC) { load_t(c + 1); ++n_t; }     // U was read: the product that read T is done
-            if (lane == 0) {
+            if (elect_one()) {                            // its second half, for the later 32 tokens
+#pragma unroll
+                for (int ks = 0; ks < 6; ++ks) {
+                    const int q = ks & 1, part = ks >> 1;
+                    umma_ts(tbase + Lay::U + 32, tbase + Lay::R + 32 + (part == 1 ? 8 : 0) + 16 * q,
+                            umma_desc(sg + Lay::T + (part == 2 ? kDlTile : 0) + 4096 + 64 + q * 32, 16, 1024), kId32, 1);
+                }
+                umma_commit(bar(Lay::U_1));
+            }
+            // the increment goes where S is: Q S^T has to be done with it
+            if (!(ok = delta_wait(bar(Lay::X_Q), c, dead) && delta_wait(bar(Lay::U_IN0), c, dead))) break;
+            tc_fence_after();
+            auto increment = [&](int half) {              // U_w^T K, 16 tokens a step, hi and lo
+#pragma unroll
+                for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                    umma_ts(tbase + Lay::DD, tbase + Lay::UW + 8 * ks, umma_desc(kt + (ks >> 1) * 2048, 8192, 1024), kIdS, ks > 0);
+            };
+            if (elect_one()) increment(0);
+            if (!(ok = delta_wait(bar(Lay::U_IN1), c, dead))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                increment(1);
+                umma_commit(bar(Lay::D));
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)            // Y += M U
-                    umma_ts(tbase + 192, tbase + 160 + 8 * ks, umma_desc(sb + Lay::M + ks * 32, 16, 1024), kIdN, 1);
-                umma_commit(bar(Lay::YM));
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)            // U_w^T K, n < 64
-                    umma_ts(tbase, tbase + 64 + 8 * ks, umma_desc(kt + (ks & 3) * 2048, 16384, 1024), kIdS, ks > 0);
-                umma_commit(bar(Lay::D_A));
+                    umma_ts(tbase + Lay::XQ + (ks >> 1) * 32, tbase + Lay::UH + 8 * ks,
+                            umma_desc(sg + Lay::M + (ks >> 1) * 4096 + ks * 32, 16, 1024), ks < 2 ? kId64 : kId32, 1);
+                umma_commit(bar(Lay::Y_M));
             }
-            // the other half of the increment takes the columns of U hi, once M U has read them
-            if (!(ok = delta_wait(bar(Lay::YM), c, dead))) break;
-            if (lane == 0 && N == 128) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    umma_ts(tbase + 128, tbase + 64 + 8 * ks, umma_desc(kt + 16384 + (ks & 3) * 2048, 16384, 1024), kIdS, ks > 0);
-                umma_commit(bar(Lay::D_B));
-            }
-            if (c + 1 < nC) { load_m(c + 1); ++n_m; }
+            if (++st == ST) { st = 0; ++use; }
         }
         if (!ok) {
             // copies and products in flight end before the block does (bounded waits)
-            if (lane == 0) {
+            if (elect_one()) {
                 atomicExch(p.err, 1);
                 umma_commit(bar(Lay::DRAIN));
             }
             __syncwarp();
             mbar_wait(bar(Lay::DRAIN), 0u);
-            if (n_kq > 0) mbar_wait(bar(Lay::FULL_KQ0 + ((n_kq - 1) & 1)), (uint32_t)((n_kq - 1) >> 1) & 1);
-            if (n_kq > 1) mbar_wait(bar(Lay::FULL_KQ0 + (n_kq & 1)), (uint32_t)((n_kq - 2) >> 1) & 1);
-            if (n_v > 0) mbar_wait(bar(Lay::FULL_V), (uint32_t)(n_v - 1) & 1);
-            if (n_t > 0) mbar_wait(bar(Lay::FULL_T), (uint32_t)(n_t - 1) & 1);
-            if (n_m > 0) mbar_wait(bar(Lay::FULL_M), (uint32_t)(n_m - 1) & 1);
+            for (int i = max(0, loaded - ST); i < loaded; ++i) mbar_wait(bar(Lay::FULL + i % ST), (uint32_t)(i / ST) & 1);
         }
-    } else if (w < WARPS) {
-        // ---------------- a thread per value column
-        const int v = tid;
-        const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
-        float S[N];                                       // lambda times the state row
-        float lam = 1.f, ilam = 1.f;                      // the lane's scale and its inverse
-        const size_t hoff = (((size_t)b * d.H + h) * P + v) * N;
+    } else if (w == 17) {
+        // ---------------- the largest |v| of each column (bf16 bits order like their values)
+        constexpr int PW = P / 64;                        // words (column pairs) a lane
+        for (int c = 0, st = 0, use = 0; c < nC; ++c) {
+            if (!delta_wait(bar(Lay::FULL + st), use, dead)) break;
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(sm + st * Lay::STAGE + Lay::V) + lane * PW;
+            const int rows = min(C, len - c * C);
+            uint32_t m[PW];
 #pragma unroll
-        for (int n = 0; n < N; n += 4) {
-            const float4 x = d.h0 ? *reinterpret_cast<const float4*>(d.h0 + hoff + n) : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[n] = x.x; S[n + 1] = x.y; S[n + 2] = x.z; S[n + 3] = x.w;
-        }
-        float mS = 0.f;
-        // multiplies the lane by 2^-e, e the exponent of m
-        auto rescale = [&](float m) {
-            const int e = exp_above(m);
-            const float f = pow2i(-e);
-            // lambda stays a float power of two whose inverse is one
-            if (lam * f < 0x1p-100f || lam * f > 0x1p100f) return 1.f;
-            lam *= f;
-            ilam *= pow2i(e);
+            for (int i = 0; i < PW; ++i) m[i] = 0;
+#pragma unroll 8
+            for (int t = 0; t < rows; ++t)
 #pragma unroll
-            for (int n = 0; n < N; ++n) S[n] *= f;
-            mS *= f;
-            return f;
-        };
-        auto store_state = [&]() {                        // S into the A operand's columns
-            mS = 0.f;
+                for (int i = 0; i < PW; ++i) m[i] = __vmaxu2(m[i], v[t * (P / 2) + i] & 0x7fff7fffu);
+            float* vm = reinterpret_cast<float*>(sm + Lay::VM) + st * P + 2 * PW * lane;
 #pragma unroll
-            for (int n = 0; n < N; n += 2) mS = max_abs3(mS, S[n], S[n + 1]);
-            if (mS > 64.f || (mS < 0.125f && mS > 0.f)) rescale(mS);
+            for (int i = 0; i < PW; ++i) *reinterpret_cast<float2*>(vm + 2 * i) = make_float2(bf16_lo(m[i]), bf16_hi(m[i]));
             __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Lay::VMAX + st));
+            if (++st == ST) { st = 0; ++use; }
+        }
+    } else if ((w & 3) < P / 32) {
+        // ---------------- four threads a value column
+        const int part = w >> 2, v = 32 * (w & 3) + lane;
+        constexpr int NQ = N / 4;                         // states of a thread: n = NQ part ..
+        const uint32_t tl = tbase + ((uint32_t)(32 * (w & 3)) << 16);
+        float2 S[NQ / 2];                                 // lambda times its part of the state row
+        float lam = 1.f, ilam = 1.f;                      // the lane's scale and its inverse
+        const size_t hoff = (((size_t)b * d.H + h) * P + v) * N + NQ * part;
 #pragma unroll
-            for (int n0 = 0; n0 < N; n0 += 16) {
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) split_f16(S[n0 + 2 * q], S[n0 + 2 * q + 1], hi[q], lo[q]);
-                tmem_st8(tl + n0 / 2, hi);
-                tmem_st8(tl + 64 + n0 / 2, lo);
-            }
-            tmem_st_wait();
-        };
+        for (int n = 0; n < NQ; n += 4) {
+            const float4 x = d.h0 ? *reinterpret_cast<const float4*>(d.h0 + hoff + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[n / 2] = make_float2(x.x, x.y);
+            S[n / 2 + 1] = make_float2(x.z, x.w);
+        }
+        float* smax = reinterpret_cast<float*>(sm + Lay::SMAX) + v;
         auto arrive = [&](int i) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(i));
         };
-        if (nC > 0) {
-            store_state();
-            arrive(Lay::S_IN);
-        }
         bool ok = true;
-        for (int c = 0; c < nC; ++c) {
-            const float* vec = reinterpret_cast<const float*>(sm + Lay::VEC + (c & 1) * kDlVec);
-            const unsigned short* sv = reinterpret_cast<const unsigned short*>(sm + Lay::V) + v;
-            const int rows = min(C, len - c * C);
-            // ---- R = V - e^Gamma rk (K S^T)
-            float fx = 1.f;                               // what the lane was rescaled by since Q S^T
-            {
-                if (!(ok = delta_wait(bar(Lay::FULL_V), c, dead) && delta_wait(bar(Lay::X_K), c, dead))) break;
-                tc_fence_after();
-                if (rows < C)                             // tokens that are not there write nothing
-                    for (int t = rows; t < C; ++t) const_cast<unsigned short*>(sv)[t * P] = 0;
-                // a lane whose values have left the window rescales and does it again
-                for (int pass = 0; pass < 2; ++pass) {
-                    float m = 0.f;
+        float yl = 0.f;                                   // what Y of the chunk before is in units of
+        for (int c = 0, st = 0, use = 0; c <= nC; ++c) {
+            const unsigned char* sg = sm + st * Lay::STAGE;
+            if (c < nC) {
+                // ---- the lane's scale for this chunk, S into the A operand's columns
+                float m = 0.f;
 #pragma unroll
-                    for (int t0 = 0; t0 < C; t0 += 16) {
-                        float x[16];
-                        tmem_ld16(tl + 128 + t0, x);
+                for (int n = 0; n < NQ / 2; ++n) m = max_abs3(m, S[n].x, S[n].y);
+                smax[128 * part] = m;
+                arrive(Lay::QUAD + (w & 3));
+                // every thread of the lane has told its largest and read its increment; V and the vectors are here
+                if (!(ok = delta_wait(bar(Lay::QUAD + (w & 3)), c, dead) && delta_wait(bar(Lay::VMAX + st), use, dead))) break;
+                m = fmaxf(fmaxf(smax[0], smax[128]), fmaxf(smax[256], smax[384]));
+                m = fmaxf(m, lam * reinterpret_cast<const float*>(sm + Lay::VM)[st * P + v]);
+                const bool out = m > 64.f || (m < 0.125f && m > 0.f);
+                if (__any_sync(0xffffffffu, out)) {
+                    const int e = out ? exp_above(m) : 0;
+                    float f = pow2i(-e);
+                    if (lam * f < 0x1p-100f || lam * f > 0x1p100f) f = 1.f;    // lambda and its inverse stay floats
+                    lam *= f;
+                    ilam = __uint_as_float(0x7f000000u - __float_as_uint(lam));  // of a power of two: exponents swapped
 #pragma unroll
-                        for (int q = 0; q < 16; q += 4) {
-                            const float4 ek = *reinterpret_cast<const float4*>(vec + t0 + q);
-                            const float e4[4] = {ek.x, ek.y, ek.z, ek.w};
+                    for (int n = 0; n < NQ / 2; ++n) S[n] = __fmul2_rn(S[n], make_float2(f, f));
+                }
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const float val = __uint_as_float((uint32_t)sv[(t0 + q + u) * P] << 16);
-                                x[q + u] = fmaf(-(e4[u] * fx), x[q + u], lam * val);
-                            }
-                        }
-                        uint32_t hi[8], lo[8];
+                for (int n0 = 0; n0 < NQ / 2; n0 += 8) {
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            m = max_abs3(m, x[2 * q], x[2 * q + 1]);
-                            split_f16(x[2 * q], x[2 * q + 1], hi[q], lo[q]);
-                        }
-                        tmem_st8(tl + 64 + t0 / 2, hi);
-                        tmem_st8(tl + 96 + t0 / 2, lo);
-                    }
-                    const float mm = fmaxf(m, mS);
-                    const bool out = m > 64.f || (mm < 0.125f && mm > 0.f);
-                    if (!__any_sync(0xffffffffu, out) || pass) break;
-                    if (out) fx = rescale(mm);
-                    __syncwarp();
+                    for (int q = 0; q < 8; ++q) split_f16(S[n0 + q], hi[q], lo[q]);
+                    tmem_st8(tl + Lay::S_HI + NQ / 2 * part + n0, hi);
+                    tmem_st8(tl + Lay::S_LO + NQ / 2 * part + n0, lo);
                 }
                 tmem_st_wait();
-                arrive(Lay::R_IN);
-            }
-            // ---- e^Gamma (Q S^T), back to its columns, while U = T R runs
-            {
-                if (!(ok = delta_wait(bar(Lay::X_Q), c, dead))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int t0 = 0; t0 < C; t0 += 16) {
-                    float x[16];
-                    uint32_t o[16];
-                    tmem_ld16(tl + 192 + t0, x);
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) {
-                        const float4 e = *reinterpret_cast<const float4*>(vec + C + t0 + q);
-                        o[q] = __float_as_uint(x[q] * (e.x * fx));
-                        o[q + 1] = __float_as_uint(x[q + 1] * (e.y * fx));
-                        o[q + 2] = __float_as_uint(x[q + 2] * (e.z * fx));
-                        o[q + 3] = __float_as_uint(x[q + 3] * (e.w * fx));
-                    }
-                    tmem_st16(tl + 192 + t0, o);
-                }
-            }
-            // ---- U: one part for Y; weighted, two parts for the state
-            {
-                if (!(ok = delta_wait(bar(Lay::UR), c, dead))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int t0 = 0; t0 < C; t0 += 16) {
-                    uint32_t u[8], hi[8], lo[8];
-                    float x[16];
-                    tmem_ld16(tl + t0, x);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) u[q] = pack_f16(x[2 * q], x[2 * q + 1]);
-                    tmem_st8(tl + 160 + t0 / 2, u);
-#pragma unroll
-                    for (int q = 0; q < 8; q += 2) {
-                        const float4 wk = *reinterpret_cast<const float4*>(vec + 2 * C + t0 + 2 * q);
-                        split_f16(x[2 * q] * wk.x, x[2 * q + 1] * wk.y, hi[q], lo[q]);
-                        split_f16(x[2 * q + 2] * wk.z, x[2 * q + 3] * wk.w, hi[q + 1], lo[q + 1]);
-                    }
-                    tmem_st8(tl + 64 + t0 / 2, hi);
-                    tmem_st8(tl + 96 + t0 / 2, lo);
-                }
-                tmem_st_wait();
-                arrive(Lay::U_IN);
-            }
-            // ---- the state after the chunk
-            const float el = vec[2 * C - 1];
-            {
-                if (!(ok = delta_wait(bar(Lay::D_A), c, dead))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int n0 = 0; n0 < 64; n0 += 16) {
-                    float x[16];
-                    tmem_ld16(tl + n0, x);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) S[n0 + q] = fmaf(el, S[n0 + q], x[q]);
-                }
-                if constexpr (N == 128) {
-                    if (!(ok = delta_wait(bar(Lay::D_B), c, dead))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int n0 = 64; n0 < 128; n0 += 16) {
-                        float x[16];
-                        tmem_ld16(tl + 64 + n0, x);
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) S[n0 + q] = fmaf(el, S[n0 + q], x[q]);
-                    }
-                }
-            }
-            const float yl = ilam;                        // Y is in units of the lane's scale so far
-            if (c + 1 < nC) {
-                store_state();
                 arrive(Lay::S_IN);
             }
-            // ---- y, while K S^T of the next chunk runs: neighbouring lanes trade
-            // tokens, so a lane stores two columns of one token
-            if (!(ok = delta_wait(bar(Lay::YM), c, dead))) break;
-            tc_fence_after();
-            const int odd = lane & 1;
-            __nv_bfloat16* yo = static_cast<__nv_bfloat16*>(d.y) + (((size_t)b * d.L + (size_t)c * C + odd) * d.H + h) * P + (v & ~1);
-            const size_t ystep = (size_t)d.H * P;
-#pragma unroll
-            for (int t0 = 0; t0 < C; t0 += 16) {
+            // ---- y of chunk c - 1, while K S^T runs: 16 tokens a thread; neighbouring
+            // lanes trade tokens, so a lane stores two columns of one token
+            if (c > 0) {
+                if (!(ok = delta_wait(bar(Lay::Y_M), c - 1, dead))) break;
+                tc_fence_after();
+                const int odd = lane & 1, t0 = (c - 1) * C + 16 * part + odd, left = len - t0;
+                const size_t ystep = 2 * (size_t)d.H * P;
+                __nv_bfloat16* yo = static_cast<__nv_bfloat16*>(d.y) + (((size_t)b * d.L + t0) * d.H + h) * P + (v & ~1);
+                const float2 yl2 = make_float2(yl, yl);
                 float x[16];
-                tmem_ld16(tl + 192 + t0, x);
+                tmem_ld16(tl + Lay::XQ + 16 * part, x);
+                arrive(Lay::Y_OUT);
+                uint32_t o[8];
 #pragma unroll
-                for (int q = 0; q < 16; q += 4) {
-                    const float4 oq = *reinterpret_cast<const float4*>(vec + 3 * C + t0 + q);
-                    x[q] *= oq.x * yl; x[q + 1] *= oq.y * yl; x[q + 2] *= oq.z * yl; x[q + 3] *= oq.w * yl;
-                }
-#pragma unroll
-                for (int q = 0; q < 16; q += 2) {
-                    const uint32_t mine = pack_bf16(x[q], x[q + 1]);
+                for (int q = 0; q < 8; ++q) {
+                    const float2 a = __fmul2_rn(make_float2(x[2 * q], x[2 * q + 1]), yl2);
+                    const uint32_t mine = pack_bf16(a.x, a.y);
                     const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-                    const uint32_t o = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-                    if (t0 + q + odd < rows) *reinterpret_cast<uint32_t*>(yo + (t0 + q) * ystep) = o;
+                    o[q] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+                }
+                if (len - (c - 1) * C >= C) {             // no token of the chunk is missing
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) *reinterpret_cast<uint32_t*>(yo + q * ystep) = o[q];
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (2 * q < left) *reinterpret_cast<uint32_t*>(yo + q * ystep) = o[q];
                 }
             }
-            arrive(Lay::Y_OUT);
+            if (c == nC) break;
+            const float* vec = reinterpret_cast<const float*>(sg + Lay::VEC);
+            const unsigned short* sv = reinterpret_cast<const unsigned short*>(sg + Lay::V) + v;
+            const unsigned short lamb = (unsigned short)(__float_as_uint(lam) >> 16);     // a power of two: exact
+            const int rows = len - c * C;                 // tokens behind them write nothing
+            yl = ilam * vec[3 * C + 1];
+            // ---- R = V - e^Gamma rk (K S^T), 8 tokens of each half a thread
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!(ok = delta_wait(bar(Lay::X_K0 + half), c, dead))) break;
+                tc_fence_after();
+                const int t0 = 32 * half + 8 * part;
+                float x[8];
+                tmem_ld8(tl + Lay::XK + t0, x);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int q = 0; q < 8; q += 4) {
+                    unsigned short vt[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        vt[u] = sv[(t0 + q + u) * P];
+                        if (t0 + q + u >= rows) vt[u] = 0;
+                    }
+                    const float4 ek = *reinterpret_cast<const float4*>(vec + t0 + q);
+                    float2 a = __fmul2_rn(make_float2(ek.x, ek.y), make_float2(x[q], x[q + 1]));
+                    float2 e = __fmul2_rn(make_float2(ek.z, ek.w), make_float2(x[q + 2], x[q + 3]));
+                    a.x = fma_bf16(vt[0], lamb, a.x);
+                    a.y = fma_bf16(vt[1], lamb, a.y);
+                    e.x = fma_bf16(vt[2], lamb, e.x);
+                    e.y = fma_bf16(vt[3], lamb, e.y);
+                    split_f16(a, hi[q / 2], lo[q / 2]);
+                    split_f16(e, hi[q / 2 + 1], lo[q / 2 + 1]);
+                }
+                const uint32_t r = tl + Lay::R + 32 * half + 16 * (part >> 1) + 4 * (part & 1);
+                tmem_st4(r, hi);
+                tmem_st4(r + 8, lo);
+                tmem_st_wait();
+                arrive(Lay::R_IN0 + half);
+            }
+            if (!ok) break;
+            // ---- e^Gamma rq (Q S^T), back to its columns, while U = T R runs
+            if (!(ok = delta_wait(bar(Lay::X_Q), c, dead))) break;
+            tc_fence_after();
+            {
+                float x[16];
+                uint32_t o[16];
+                tmem_ld16(tl + Lay::XQ + 16 * part, x);
+#pragma unroll
+                for (int q = 0; q < 16; q += 4) {
+                    const float4 e = *reinterpret_cast<const float4*>(vec + C + 16 * part + q);
+                    const float2 a = __fmul2_rn(make_float2(e.x, e.y), make_float2(x[q], x[q + 1]));
+                    const float2 f = __fmul2_rn(make_float2(e.z, e.w), make_float2(x[q + 2], x[q + 3]));
+                    o[q] = __float_as_uint(a.x); o[q + 1] = __float_as_uint(a.y);
+                    o[q + 2] = __float_as_uint(f.x); o[q + 3] = __float_as_uint(f.y);
+                }
+                tmem_st16(tl + Lay::XQ + 16 * part, o);
+            }
+            // ---- U: one part for Y; weighted, two parts for the state
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!(ok = delta_wait(bar(Lay::U_0 + half), c, dead))) break;
+                tc_fence_after();
+                const int t0 = 32 * half + 8 * part;
+                float x[8];
+                tmem_ld8(tl + Lay::U + t0, x);
+                uint32_t u[4], hi[4], lo[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) u[q] = pack_f16(x[2 * q], x[2 * q + 1]);
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    const float4 wk = *reinterpret_cast<const float4*>(vec + 2 * C + t0 + 2 * q);
+                    split_f16(__fmul2_rn(make_float2(x[2 * q], x[2 * q + 1]), make_float2(wk.x, wk.y)), hi[q], lo[q]);
+                    split_f16(__fmul2_rn(make_float2(x[2 * q + 2], x[2 * q + 3]), make_float2(wk.z, wk.w)), hi[q + 1], lo[q + 1]);
+                }
+                const uint32_t r = tl + Lay::UW + 32 * half + 16 * (part >> 1) + 4 * (part & 1);
+                tmem_st4(r, hi);
+                tmem_st4(r + 8, lo);
+                tmem_st4(tl + Lay::UH + t0 / 2, u);
+                tmem_st_wait();
+                arrive(Lay::U_IN0 + half);
+            }
+            if (!ok) break;
+            // ---- the state after the chunk
+            const float el = vec[3 * C];
+            const float2 el2 = make_float2(el, el);
+            if (!(ok = delta_wait(bar(Lay::D), c, dead))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int n0 = 0; n0 < NQ; n0 += 16) {
+                float x[16];
+                tmem_ld16(tl + Lay::DD + NQ * part + n0, x);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) S[n0 / 2 + q] = __ffma2_rn(el2, S[n0 / 2 + q], make_float2(x[2 * q], x[2 * q + 1]));
+            }
+            if (++st == ST) { st = 0; ++use; }
         }
         if (ok) {
 #pragma unroll
-            for (int n = 0; n < N; n += 4)
+            for (int n = 0; n < NQ; n += 4)
                 *reinterpret_cast<float4*>(d.h_out + hoff + n) =
-                    make_float4(S[n] * ilam, S[n + 1] * ilam, S[n + 2] * ilam, S[n + 3] * ilam);
+                    make_float4(S[n / 2].x * ilam, S[n / 2].y * ilam, S[n / 2 + 1].x * ilam, S[n / 2 + 1].y * ilam);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == 4 && !*dead) tmem_dealloc(tbase, Lay::COLS);   // a late product must not meet another block's columns
+    if (w == 16 && !*dead) tmem_dealloc(tbase, Lay::COLS);   // a late product must not meet another block's columns
 }
 
 }  // namespace axon
