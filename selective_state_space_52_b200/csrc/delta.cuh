@@ -74,15 +74,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 // A pair as hi + lo fp16 parts: hi the leading 11 bits (cut off, so that the
-// rest is one exact subtraction), lo the rest rounded.  Five instructions a
-// pair; with hi rounded instead, converting it back to subtract it took half
-// as long again.
+// rest is an exact subtraction), lo the rest rounded.  8.1 cycles a pair and
+// warp; rounding hi and subtracting it in the mixed precision fma took 9.6.
 __device__ __forceinline__ void split_f16(float2 x, uint32_t& hi, uint32_t& lo) {
-    const float2 h = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffffe000u),
-                                 __uint_as_float(__float_as_uint(x.y) & 0xffffe000u));
-    const float2 r = __ffma2_rn(h, make_float2(-1.0f, -1.0f), x);
-    hi = pack_f16(h.x, h.y);
-    lo = pack_f16(r.x, r.y);
+    const float h0 = __uint_as_float(__float_as_uint(x.x) & 0xffffe000u), h1 = __uint_as_float(__float_as_uint(x.y) & 0xffffe000u);
+    hi = pack_f16(h0, h1);
+    lo = pack_f16(x.x - h0, x.y - h1);
 }
 // a b + c with a and b in bf16
 __device__ __forceinline__ float fma_bf16(unsigned short a, unsigned short b, float c) {
@@ -502,7 +499,9 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
     const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(sm + Lay::SLOT);
 
     if (w == 16) {
-        // ---------------- copies and products
+        // ---------------- copies and products.  The warp runs the loop together and one
+        // lane issues: in a region of one lane only, addresses live in vector
+        // registers, and a product costs twice what the tensor core takes for it.
         const unsigned char* kq = p.kq + ((size_t)b * d.G + g) * p.nC * (2 * Lay::K_BYTES);
         const unsigned char* blob = p.blob + ((size_t)b * d.H + h) * p.nC * kDlBlob;
         auto load_chunk = [&](int c, int st) {            // V's rows past L read as zeros
@@ -520,10 +519,15 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
         constexpr uint32_t kId64 = umma_idesc_f16(128, 64, 0, 0);    // B K-major: K', Q', T, M rows
         constexpr uint32_t kId32 = umma_idesc_f16(128, 32, 0, 0);
         constexpr uint32_t kIdS = umma_idesc_f16(128, N, 0, 1);      // B: K' rows as the K dimension (MN-major)
-        auto rows_desc = [&](uint32_t t, int ks) { return umma_desc(t + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024); };
+        // matrix descriptors of the first stage; an offset within shared memory
+        // adds to their address field, so a step costs one addition
+        const uint64_t d_k = umma_desc(sb + Lay::K, 16, 1024), d_ks = umma_desc(sb + Lay::K, 8192, 1024);
+        auto at = [](uint64_t desc, int bytes) { return desc + (uint64_t)(bytes >> 4); };
+        auto rows = [](int ks) { return (ks >> 2) * 8192 + (ks & 3) * 32; };     // K step ks of a 64-row tile
+        const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
         bool ok = true;
         for (int c = 0, st = 0, use = 0; c < nC; ++c) {
-            const uint32_t sg = sb + st * Lay::STAGE, kt = sg + Lay::K, qt = sg + Lay::Q;
+            const uint64_t k_d = d_k + (uint64_t)(st * (Lay::STAGE >> 4)), ks_d = d_ks + (uint64_t)(st * (Lay::STAGE >> 4));
             if (!(ok = delta_wait(bar(Lay::FULL + st), use, dead) && delta_wait(bar(Lay::S_IN), c, dead))) break;
             tc_fence_after();
             if (elect_one()) {                            // K S^T, both parts of S, 32 tokens at a time
@@ -531,22 +535,23 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 for (int half = 0; half < 2; ++half) {
 #pragma unroll
                     for (int ks = 0; ks < 2 * KS; ++ks)
-                        umma_ts(tbase + Lay::XK + 32 * half, tbase + (ks / KS) * Lay::S_LO + 8 * (ks % KS),
-                                rows_desc(kt + 4096 * half, ks % KS), kId32, ks > 0);
+                        umma_ts(tb + Lay::XK + 32 * half, tb + (ks / KS) * Lay::S_LO + 8 * (ks % KS),
+                                at(k_d, 4096 * half + rows(ks % KS)), kId32, ks > 0);
                     umma_commit(bar(Lay::X_K0 + half));
                 }
             }
             if (!(ok = c == 0 || delta_wait(bar(Lay::Y_OUT), c - 1, dead))) break;
             tc_fence_after();
+            if (elect_one()) {                            // Q S^T, the hi part
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    umma_ts(tb + Lay::XQ, tb + Lay::S_HI + 8 * ks, at(k_d, Lay::Q + rows(ks)), kId64, ks > 0);
+                umma_commit(bar(Lay::X_Q));
+            }
             // chunk c - 1 is done with its stage: its increment and its Y have been read
             if (c > 0 && loaded < nC) {
                 load_chunk(loaded, st == 0 ? ST - 1 : st - 1);
                 ++loaded;
-            }
-            if (elect_one()) {                            // Q S^T, the hi part
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) umma_ts(tbase + Lay::XQ, tbase + Lay::S_HI + 8 * ks, rows_desc(qt, ks), kId64, ks > 0);
-                umma_commit(bar(Lay::X_Q));
             }
             if (!(ok = delta_wait(bar(Lay::R_IN0), c, dead))) break;
             tc_fence_after();
@@ -554,8 +559,8 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
 #pragma unroll
                 for (int ks = 0; ks < 6; ++ks) {
                     const int q = ks & 1, part = ks >> 1;
-                    umma_ts(tbase + Lay::U, tbase + Lay::R + (part == 1 ? 8 : 0) + 16 * q,
-                            umma_desc(sg + Lay::T + (part == 2 ? kDlTile : 0) + q * 32, 16, 1024), kId64, ks > 0);
+                    umma_ts(tb + Lay::U, tb + Lay::R + (part & 1) * 8 + 16 * q, at(k_d, Lay::T + (part >> 1) * kDlTile + q * 32),
+                            kId64, ks > 0);
                 }
                 umma_commit(bar(Lay::U_0));
             }
@@ -565,8 +570,8 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
 #pragma unroll
                 for (int ks = 0; ks < 6; ++ks) {
                     const int q = ks & 1, part = ks >> 1;
-                    umma_ts(tbase + Lay::U + 32, tbase + Lay::R + 32 + (part == 1 ? 8 : 0) + 16 * q,
-                            umma_desc(sg + Lay::T + (part == 2 ? kDlTile : 0) + 4096 + 64 + q * 32, 16, 1024), kId32, 1);
+                    umma_ts(tb + Lay::U + 32, tb + Lay::R + 32 + (part & 1) * 8 + 16 * q,
+                            at(k_d, Lay::T + (part >> 1) * kDlTile + 4096 + 64 + q * 32), kId32, 1);
                 }
                 umma_commit(bar(Lay::U_1));
             }
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             auto increment = [&](int half) {              // U_w^T K, 16 tokens a step, hi and lo
 #pragma unroll
                 for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                    umma_ts(tbase + Lay::DD, tbase + Lay::UW + 8 * ks, umma_desc(kt + (ks >> 1) * 2048, 8192, 1024), kIdS, ks > 0);
+                    umma_ts(tb + Lay::DD, tb + Lay::UW + 8 * ks, at(ks_d, (ks >> 1) * 2048), kIdS, ks > 0);
             };
             if (elect_one()) increment(0);
             if (!(ok = delta_wait(bar(Lay::U_IN1), c, dead))) break;
@@ -586,8 +591,8 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 umma_commit(bar(Lay::D));
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)            // Y += M U
-                    umma_ts(tbase + Lay::XQ + (ks >> 1) * 32, tbase + Lay::UH + 8 * ks,
-                            umma_desc(sg + Lay::M + (ks >> 1) * 4096 + ks * 32, 16, 1024), ks < 2 ? kId64 : kId32, 1);
+                    umma_ts(tb + Lay::XQ + (ks >> 1) * 32, tb + Lay::UH + 8 * ks, at(k_d, Lay::M + (ks >> 1) * 4096 + ks * 32),
+                            ks < 2 ? kId64 : kId32, 1);
                 umma_commit(bar(Lay::Y_M));
             }
             if (++st == ST) { st = 0; ++use; }
@@ -602,6 +607,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             mbar_wait(bar(Lay::DRAIN), 0u);
             for (int i = max(0, loaded - ST); i < loaded; ++i) mbar_wait(bar(Lay::FULL + i % ST), (uint32_t)(i / ST) & 1);
         }
+        __syncwarp();
     } else if (w == 17) {
         // ---------------- the largest |v| of each column (bf16 bits order like their values)
         constexpr int PW = P / 64;                        // words (column pairs) a lane
@@ -648,12 +654,16 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
         for (int c = 0, st = 0, use = 0; c <= nC; ++c) {
             const unsigned char* sg = sm + st * Lay::STAGE;
             if (c < nC) {
-                // ---- the lane's scale for this chunk, S into the A operand's columns
+                // ---- the lane's scale for this chunk, S into the A operand's columns:
+                // first in the scale it has, which nearly always stands
                 float m = 0.f;
 #pragma unroll
                 for (int n = 0; n < NQ / 2; ++n) m = max_abs3(m, S[n].x, S[n].y);
                 smax[128 * part] = m;
                 arrive(Lay::QUAD + (w & 3));
+                uint32_t hi[NQ / 2], lo[NQ / 2];
+#pragma unroll
+                for (int q = 0; q < NQ / 2; ++q) split_f16(S[q], hi[q], lo[q]);
                 // every thread of the lane has told its largest and read its increment; V and the vectors are here
                 if (!(ok = delta_wait(bar(Lay::QUAD + (w & 3)), c, dead) && delta_wait(bar(Lay::VMAX + st), use, dead))) break;
                 m = fmaxf(fmaxf(smax[0], smax[128]), fmaxf(smax[256], smax[384]));
@@ -666,15 +676,15 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                     lam *= f;
                     ilam = __uint_as_float(0x7f000000u - __float_as_uint(lam));  // of a power of two: exponents swapped
 #pragma unroll
-                    for (int n = 0; n < NQ / 2; ++n) S[n] = __fmul2_rn(S[n], make_float2(f, f));
+                    for (int q = 0; q < NQ / 2; ++q) {
+                        S[q] = __fmul2_rn(S[q], make_float2(f, f));
+                        split_f16(S[q], hi[q], lo[q]);
+                    }
                 }
 #pragma unroll
                 for (int n0 = 0; n0 < NQ / 2; n0 += 8) {
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) split_f16(S[n0 + q], hi[q], lo[q]);
-                    tmem_st8(tl + Lay::S_HI + NQ / 2 * part + n0, hi);
-                    tmem_st8(tl + Lay::S_LO + NQ / 2 * part + n0, lo);
+                    tmem_st8(tl + Lay::S_HI + NQ / 2 * part + n0, reinterpret_cast<uint32_t(&)[8]>(hi[n0]));
+                    tmem_st8(tl + Lay::S_LO + NQ / 2 * part + n0, reinterpret_cast<uint32_t(&)[8]>(lo[n0]));
                 }
                 tmem_st_wait();
                 arrive(Lay::S_IN);
@@ -715,29 +725,31 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             const int rows = len - c * C;                 // tokens behind them write nothing
             yl = ilam * vec[3 * C + 1];
             // ---- R = V - e^Gamma rk (K S^T), 8 tokens of each half a thread
-#pragma unroll
+#pragma unroll 1
             for (int half = 0; half < 2; ++half) {
+                const int t0 = 32 * half + 8 * part;
+                unsigned short vt[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) vt[q] = sv[(t0 + q) * P];
+                if (t0 + 8 > rows) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (t0 + q >= rows) vt[q] = 0;
+                }
                 if (!(ok = delta_wait(bar(Lay::X_K0 + half), c, dead))) break;
                 tc_fence_after();
-                const int t0 = 32 * half + 8 * part;
                 float x[8];
                 tmem_ld8(tl + Lay::XK + t0, x);
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int q = 0; q < 8; q += 4) {
-                    unsigned short vt[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        vt[u] = sv[(t0 + q + u) * P];
-                        if (t0 + q + u >= rows) vt[u] = 0;
-                    }
                     const float4 ek = *reinterpret_cast<const float4*>(vec + t0 + q);
                     float2 a = __fmul2_rn(make_float2(ek.x, ek.y), make_float2(x[q], x[q + 1]));
                     float2 e = __fmul2_rn(make_float2(ek.z, ek.w), make_float2(x[q + 2], x[q + 3]));
-                    a.x = fma_bf16(vt[0], lamb, a.x);
-                    a.y = fma_bf16(vt[1], lamb, a.y);
-                    e.x = fma_bf16(vt[2], lamb, e.x);
-                    e.y = fma_bf16(vt[3], lamb, e.y);
+                    a.x = fma_bf16(vt[q + 0], lamb, a.x);
+                    a.y = fma_bf16(vt[q + 1], lamb, a.y);
+                    e.x = fma_bf16(vt[q + 2], lamb, e.x);
+                    e.y = fma_bf16(vt[q + 3], lamb, e.y);
                     split_f16(a, hi[q / 2], lo[q / 2]);
                     split_f16(e, hi[q / 2 + 1], lo[q / 2 + 1]);
                 }
@@ -766,7 +778,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 tmem_st16(tl + Lay::XQ + 16 * part, o);
             }
             // ---- U: one part for Y; weighted, two parts for the state
-#pragma unroll
+#pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 if (!(ok = delta_wait(bar(Lay::U_0 + half), c, dead))) break;
                 tc_fence_after();
