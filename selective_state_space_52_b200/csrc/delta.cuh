@@ -107,65 +107,107 @@ __device__ __forceinline__ int exp_above(float m) {
     return min(max(e, -100), 100);
 }
 
-// ---- prep: grid = (nC, G, B), 128 threads
+// ---- prep: grid = (nC, G, B), 128 threads.  What bounds it is latency and the
+// instruction caches (five blocks an SM in different phases), so the loops are
+// kept short: forward substitution down whole columns, unrolled over
+// registers, took 15 to 24 thousand cycles a head where this takes three.
 template <int N>
 struct DeltaPrepSmem {
     static constexpr int LDA = 68;                       // floats a row of A: 16-byte rows without bank conflicts
-    static constexpr int KQ = 0;                         // [K'; Q'] tile, read by the Gram products only ...
-    static constexpr int A = 0;                          // ... then A (float32), later the T parts over it
-    static constexpr int M = kDlC * LDA * 4;             // M tile
+    static constexpr int LDW = 36;
     static constexpr int KQ_BYTES = 128 * N * 2;
-    static constexpr int V = KQ_BYTES > M + kDlTile ? KQ_BYTES : M + kDlTile;   // the vectors
-    static constexpr int RK = V + kDlVec;                // rk'
+    static constexpr int KQ = 0;                         // [K'; Q'] tile, read by the Gram products only ...
+    static constexpr int A = 0;                          // ... then A (float32), in place (I + A)^-1,
+    static constexpr int M = kDlC * LDA * 4;             // the M tile,
+    static constexpr int W = M + kDlTile;                // and a product on its way
+    static constexpr int W_END = W + 32 * LDW * 4;
+    static constexpr int V = KQ_BYTES > W_END ? KQ_BYTES : W_END;   // the vectors, two heads
+    static constexpr int RK = V + 2 * kDlVec;            // rk'
     static constexpr int RQ = RK + kDlC * 4;             // rq', the largest in [1/2, 1)
-    static constexpr int GH = RQ + kDlC * 4;             // Gamma (log2 units), float hi and lo parts
-    static constexpr int GL = GH + kDlC * 4;
-    static constexpr int BE = GL + kDlC * 4;             // beta
-    static constexpr int TOT = BE + kDlC * 4;            // double: the first warp's total
-    static constexpr int MB = TOT + 8;
+    static constexpr int GH = RQ + kDlC * 4;             // two heads: Gamma (log2 units), float hi and lo parts
+    static constexpr int GL = GH + 2 * kDlC * 4;
+    static constexpr int BE = GL + 2 * kDlC * 4;         // beta
+    static constexpr int VJ = BE + 2 * kDlC * 4;         // e^(Gamma_r - Gamma_j) rk'_j, r the last of j's 16 tokens
+    static constexpr int TOT = VJ + 2 * kDlC * 4;        // doubles: the first warps' totals
+    static constexpr int MB = TOT + 16;
     static constexpr int SLOT = MB + 8;
     static constexpr int YS = SLOT + 4;                  // scale times what RQ was divided by
     static constexpr int BYTES = YS + 4;
     static constexpr int TOTAL = BYTES + 1024;           // with the alignment pad
-    static_assert(2 * kDlTile <= M, "the T parts fit over A");
-    static_assert(M % 16 == 0 && V % 16 == 0 && TOT % 8 == 0, "alignment");
+    static_assert(M % 16 == 0 && W % 16 == 0 && V % 16 == 0 && TOT % 8 == 0, "alignment");
 };
 
-// Column j of (I + A)^-1 for the lanes of warps 0 and 1 (j = tid): forward
-// substitution down the rows, two products per instruction; A rows are read
-// as broadcasts.  Columns of warp 1 are zero above row 32.
-__device__ __forceinline__ void delta_invert_column(const float* A, int lda, int j, bool low, float2 (&t)[kDlC / 2]) {
+// (I + A)^-1 in place, A strictly lower triangular with zeros above: 16 x 16
+// diagonal blocks by forward substitution (a thread a column), then twice
+// T21 = -T22 (A21 T11) for blocks of 16 and of 32.  128 threads; ends synchronised.
+template <int LDA, int LDW>
+__device__ __forceinline__ void delta_invert(float* A, float* W, int tid) {
+    if (tid < kDlC) {
+        const int o = tid & ~15, j = tid & 15;
+        float t[16];
 #pragma unroll
-    for (int i = 0; i < kDlC / 2; ++i) t[i] = make_float2(0.f, 0.f);
+        for (int i = 0; i < 16; ++i) {
+            const float* row = A + (o + i) * LDA + o;
+            float acc = i == j ? 1.f : 0.f;
 #pragma unroll
-    for (int i = 0; i < kDlC; ++i) {
-        float2 acc = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-        const float* row = A + i * lda;
-        if (low || i >= 32) {
-            // pairs (k, k + 1) with k < i; A_ii is 0 and the t behind row i are still 0
-            if (low) {
+            for (int k = 0; k < i; ++k) acc = fmaf(-row[k], t[k], acc);
+            t[i] = acc;
+        }
+        __syncwarp();
 #pragma unroll
-                for (int k = 0; k < (i < 32 ? i : 32); k += 4) {
-                    const float4 a = *reinterpret_cast<const float4*>(row + k);
-                    acc = __ffma2_rn(make_float2(a.x, a.y), t[k / 2], acc);
-                    if (k + 2 < i) acc1 = __ffma2_rn(make_float2(a.z, a.w), t[k / 2 + 1], acc1);
-                }
+        for (int i = 0; i < 16; ++i) A[(o + i) * LDA + o + j] = t[i];
+    }
+    __syncthreads();
+    {
+        const int o = 32 * (tid >> 6), r = (tid & 63) >> 2, c = (tid & 3) * 4;
+        float* w = W + (tid >> 6) * 16 * LDW;
+        float* row = A + (o + 16 + r) * LDA + o;         // of A21, then of T22 16 columns on
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+            const float x = row[k];
+            const float4 y = *reinterpret_cast<const float4*>(A + (o + k) * LDA + o + c);
+            s.x = fmaf(x, y.x, s.x); s.y = fmaf(x, y.y, s.y); s.z = fmaf(x, y.z, s.z); s.w = fmaf(x, y.w, s.w);
+        }
+        *reinterpret_cast<float4*>(w + r * LDW + c) = s;
+        __syncthreads();
+        s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+            const float x = -row[16 + k];
+            const float4 y = *reinterpret_cast<const float4*>(w + k * LDW + c);
+            s.x = fmaf(x, y.x, s.x); s.y = fmaf(x, y.y, s.y); s.z = fmaf(x, y.z, s.z); s.w = fmaf(x, y.w, s.w);
+        }
+        *reinterpret_cast<float4*>(row + c) = s;
+    }
+    __syncthreads();
+    {
+        const int r = tid >> 2, c = (tid & 3) * 8;
+        float* row = A + (32 + r) * LDA;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {           // W = A21 T11, then T21 = -T22 W
+            float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            const float* x = row + 32 * pass;
+            const float* y = pass ? W + c : A + c;
+            const int ldy = pass ? LDW : LDA;
+#pragma unroll 4
+            for (int k = 0; k < 32; ++k) {
+                const float xv = x[k];
+                const float4 y0 = *reinterpret_cast<const float4*>(y + k * ldy), y1 = *reinterpret_cast<const float4*>(y + k * ldy + 4);
+                s[0] = fmaf(xv, y0.x, s[0]); s[1] = fmaf(xv, y0.y, s[1]); s[2] = fmaf(xv, y0.z, s[2]); s[3] = fmaf(xv, y0.w, s[3]);
+                s[4] = fmaf(xv, y1.x, s[4]); s[5] = fmaf(xv, y1.y, s[5]); s[6] = fmaf(xv, y1.z, s[6]); s[7] = fmaf(xv, y1.w, s[7]);
             }
-#pragma unroll
-            for (int k = 32; k < i; k += 4) {
-                const float4 a = *reinterpret_cast<const float4*>(row + k);
-                acc = __ffma2_rn(make_float2(a.x, a.y), t[k / 2], acc);
-                if (k + 2 < i) acc1 = __ffma2_rn(make_float2(a.z, a.w), t[k / 2 + 1], acc1);
-            }
-            const float v = (i == j ? 1.f : 0.f) - ((acc.x + acc.y) + (acc1.x + acc1.y));
-            if (i & 1) t[i / 2].y = v;
-            else t[i / 2].x = v;
+            const float f = pass ? -1.f : 1.f;
+            float* out = pass ? row + c : W + r * LDW + c;
+            *reinterpret_cast<float4*>(out) = make_float4(f * s[0], f * s[1], f * s[2], f * s[3]);
+            *reinterpret_cast<float4*>(out + 4) = make_float4(f * s[4], f * s[5], f * s[6], f * s[7]);
+            __syncthreads();
         }
     }
 }
 
 template <int N>
-__global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
+__global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) {
     using Lay = DeltaPrepSmem<N>;
     constexpr int C = kDlC;
     grid_dep_launch();
@@ -184,72 +226,68 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
     const uint32_t sb = raw + pad;
     float* rk = reinterpret_cast<float*>(sm + Lay::RK);
     float* rq = reinterpret_cast<float*>(sm + Lay::RQ);
+
+    // ---- rows of K (tile rows 0 .. 63) and Q (64 .. 127) into the tile, eight
+    // lanes a row; rows past the end as zeros
+    constexpr int PC = N / 64;                           // 16-byte pieces of a lane
+    const int l = tid & 7, r0 = tid >> 3;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int t = r0 + 16 * (k & 3), s = k >> 2, ld = s ? d.ldq : d.ldk;
+        const bool ok = t0 + t < len;
+        const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(s ? d.q : d.k) +
+                                   ((size_t)b * d.L + (ok ? t0 + t : 0)) * ld + (size_t)g * N;
+#pragma unroll
+        for (int i = 0; i < PC; ++i)
+            cp_async16(sm + Lay::KQ + i * 16384 + (64 * s + t) * 128 + ((l ^ (t & 7)) << 4), row + 8 * (l + 8 * i), ok);
+    }
+    cp_async_commit();
     if (w == 0) tmem_alloc(sb + Lay::SLOT, 64);
     if (tid == 0) mbar_init(sb + Lay::MB, 1);
-
-    // ---- rows of K (tile rows 0 .. 63) and Q (64 .. 127): eight lanes a row,
-    // its largest element to [1/2, 1), fp16 into the tile and to global memory
-    {
-        constexpr int PC = N / 64;                       // 16-byte pieces of a lane
-        const int l = tid & 7, r0 = tid >> 3;
-        const __nv_bfloat16* base[2] = {
-            static_cast<const __nv_bfloat16*>(d.k) + (size_t)b * d.L * d.ldk + (size_t)g * N,
-            static_cast<const __nv_bfloat16*>(d.q) + (size_t)b * d.L * d.ldq + (size_t)g * N};
-        const int ld[2] = {d.ldk, d.ldq};
-        uint4 v[8][PC];
+    cp_async_wait_0();
+    // each piece in place (its own thread's): the row's largest element to [1/2, 1), fp16
+    unsigned char* kq = p.kq + (((size_t)b * d.G + g) * p.nC + c) * Lay::KQ_BYTES;
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+        const int t = r0 + 16 * (k & 3), s = k >> 2;
+        const int in_row = (l ^ (t & 7)) << 4;
+        float m = 0.f;
+        float f[PC][8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = r0 + 16 * k, t = t0 + (r & 63), s = k >> 2;
+        for (int i = 0; i < PC; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(sm + Lay::KQ + i * 16384 + (64 * s + t) * 128 + in_row);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < PC; ++i)
-                v[k][i] = t < len ? __ldg(reinterpret_cast<const uint4*>(base[s] + (size_t)t * ld[s]) + l + 8 * i)
-                                  : make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 4; ++e) {
+                f[i][2 * e] = bf16_lo(u[e]);
+                f[i][2 * e + 1] = bf16_hi(u[e]);
+                m = max_abs3(m, f[i][2 * e], f[i][2 * e + 1]);
+            }
         }
-        unsigned char* out = p.kq + (((size_t)b * d.G + g) * p.nC + c) * Lay::KQ_BYTES;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = r0 + 16 * k;
-            float m = 0.f;
-            float f[PC][8];
+        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int e = exp_above(m);
+        const float sc = pow2i(-e);
+        float ss = 0.f;
 #pragma unroll
-            for (int i = 0; i < PC; ++i) {
-                const uint32_t u[4] = {v[k][i].x, v[k][i].y, v[k][i].z, v[k][i].w};
+        for (int i = 0; i < PC; ++i) {
+            uint32_t h[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[i][2 * e] = bf16_lo(u[e]);
-                    f[i][2 * e + 1] = bf16_hi(u[e]);
-                    m = max_abs3(m, f[i][2 * e], f[i][2 * e + 1]);
-                }
+            for (int q = 0; q < 4; ++q) {
+                const float x0 = f[i][2 * q] * sc, x1 = f[i][2 * q + 1] * sc;
+                ss = fmaf(x0, x0, fmaf(x1, x1, ss));
+                h[q] = pack_f16(x0, x1);
             }
+            const uint4 o = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(sm + Lay::KQ + i * 16384 + (64 * s + t) * 128 + in_row) = o;
+            *reinterpret_cast<uint4*>(kq + s * (Lay::KQ_BYTES / 2) + i * 8192 + t * 128 + in_row) = o;
+        }
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const int e = exp_above(m);
-            const float sc = pow2i(-e);
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < PC; ++i) {
-                uint32_t h[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float x0 = f[i][2 * q] * sc, x1 = f[i][2 * q + 1] * sc;
-                    ss = fmaf(x0, x0, fmaf(x1, x1, ss));
-                    h[q] = pack_f16(x0, x1);
-                }
-                const int pc = l + 8 * i;
-                const int in_row = ((pc & 7) ^ (r & 7)) << 4;
-                const uint4 o = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(sm + Lay::KQ + (pc >> 3) * 16384 + r * 128 + in_row) = o;
-                *reinterpret_cast<uint4*>(out + (r >> 6) * (Lay::KQ_BYTES / 2) + (pc >> 3) * 8192 + (r & 63) * 128 + in_row) = o;
-            }
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (l == 0) {
-                // 1 / sqrt(|k|^2 + eps) in the scaled row's units: |k|^2 = ss 4^e
-                const float es = pow2i(e);
-                const float f1 = d.norm ? es * rsqrtf(fmaf(ss * es, es, kDeltaEps)) : es;
-                if (r < C) rk[r] = f1;
-                else rq[r - C] = f1;
-            }
+        for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (l == 0) {
+            // 1 / sqrt(|k|^2 + eps) in the scaled row's units: |k|^2 = ss 4^e
+            const float es = pow2i(e);
+            (s ? rq : rk)[t] = d.norm ? es * rsqrtf(fmaf(ss * es, es, kDeltaEps)) : es;
         }
     }
     fence_async_smem();
@@ -257,7 +295,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(sm + Lay::SLOT);
-    if (tid == 0) {
+    if (w == 0 && elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < N / 16; ++ks) {
             const uint64_t dsc = umma_desc(sb + Lay::KQ + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024);
@@ -265,6 +303,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
         }
         umma_commit(sb + Lay::MB);
     }
+    __syncwarp();
     if (w == 3) {                                        // rq' to [1/2, 1), the rest of it to the outputs' scale
         float m = fmaxf(rq[lane], rq[lane + 32]);
 #pragma unroll
@@ -275,72 +314,98 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
         if (lane == 0) *reinterpret_cast<float*>(sm + Lay::YS) = d.scale * pow2i(e);
     }
     const bool ok = mbar_wait(sb + Lay::MB, 0u);
-    const bool failed = __syncthreads_or(!ok);           // KQ is free from here on: A and M lie over it
+    const bool failed = __syncthreads_or(!ok);           // KQ is free from here on: A, M and W lie over it
     tc_fence_after();
     if (failed && tid == 0) atomicExch(p.err, 1);
 
     const int r = d.H / d.G;
     const int i = tid & 63;                              // this thread's row of A (warps 0, 1) or M (2, 3)
     const bool live = t0 + i < len;
-    float* vec = reinterpret_cast<float*>(sm + Lay::V);
-    float* gh = reinterpret_cast<float*>(sm + Lay::GH);
-    float* gl = reinterpret_cast<float*>(sm + Lay::GL);
-    float* be = reinterpret_cast<float*>(sm + Lay::BE);
     float* A = reinterpret_cast<float*>(sm + Lay::A);
+#pragma unroll 1
     for (int hh = 0; hh < r && !failed; ++hh) {
-        const int h = g * r + hh;
-        // ---- rates: warps 0 and 1, a token a lane.  The running log decay is
-        // summed in double: it reaches hundreds, and differences of neighbours count.
-        double G = 0.0;
-        if (w < 2) {
+        const int h = g * r + hh, slot = hh & 1;
+        float* vec = reinterpret_cast<float*>(sm + Lay::V) + slot * 4 * C;
+        const float* gh = reinterpret_cast<const float*>(sm + Lay::GH) + slot * C;
+        const float* gl = reinterpret_cast<const float*>(sm + Lay::GL) + slot * C;
+        const float* be = reinterpret_cast<const float*>(sm + Lay::BE) + slot * C;
+        const float* vj = reinterpret_cast<const float*>(sm + Lay::VJ) + slot * C;
+        if (slot == 0) {
+            // ---- the rates of two heads (warps 0, 1 and 2, 3), a token a lane.  The
+            // running log decay is summed in double: it reaches hundreds, and
+            // differences of neighbours count.
+            const int mine = tid >> 6, hm = h + mine;
+            const bool have = hh + mine < r;
             float lg = 0.f, beta = 0.f;
-            if (live) {
-                const size_t o = ((size_t)b * d.L + t0 + i) * d.H + h;
-                lg = delta_log2_decay(IoBF16::load(static_cast<const __nv_bfloat16*>(d.dt_raw) + o) + __ldg(d.dt_bias + h),
-                                      delta_exp_a(__ldg(d.A_log + h)));
+            if (live && have) {
+                const size_t o = ((size_t)b * d.L + t0 + i) * d.H + hm;
+                lg = delta_log2_decay(IoBF16::load(static_cast<const __nv_bfloat16*>(d.dt_raw) + o) + __ldg(d.dt_bias + hm),
+                                      delta_exp_a(__ldg(d.A_log + hm)));
                 // a decay below 2^-2000 is 0 to a float anyway, and an infinite one would leave inf - inf
                 lg = lg < -2000.f ? -2000.f : lg;
                 beta = delta_beta(IoBF16::load(static_cast<const __nv_bfloat16*>(d.b_raw) + o));
             }
-            G = (double)lg;
+            double G = (double)lg;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const double v = __shfl_up_sync(0xffffffffu, G, o);
                 if (lane >= o) G += v;
             }
-            if (tid == 31) *reinterpret_cast<double*>(sm + Lay::TOT) = G;
-            be[i] = beta;
+            double* tot = reinterpret_cast<double*>(sm + Lay::TOT) + mine;
+            float* gh2 = reinterpret_cast<float*>(sm + Lay::GH) + mine * C;
+            float* gl2 = reinterpret_cast<float*>(sm + Lay::GL) + mine * C;
+            if ((tid & 63) == 31) *tot = G;
+            reinterpret_cast<float*>(sm + Lay::BE)[mine * C + i] = beta;
+            __syncthreads();
+            if (w & 1) G += *tot;
+            const float hi = (float)G, lo = (float)(G - (double)hi);
+            gh2[i] = hi;
+            gl2[i] = lo;
+            __syncthreads();
+            const int r16 = i | 15;
+            const float eg = ex2_approx(hi);
+            float* v2 = reinterpret_cast<float*>(sm + Lay::V) + mine * 4 * C;
+            reinterpret_cast<float*>(sm + Lay::VJ)[mine * C + i] = ex2_approx((gh2[r16] - hi) + (gl2[r16] - lo)) * rk[i];
+            v2[i] = -eg * rk[i];
+            v2[C + i] = eg * rq[i];
+            v2[2 * C + i] = ex2_approx((gh2[C - 1] - hi) + (gl2[C - 1] - lo)) * rk[i];
+            if (i == C - 1) v2[3 * C] = eg;
+            if (i == 0) v2[3 * C + 1] = *reinterpret_cast<const float*>(sm + Lay::YS);
+            __syncthreads();
         }
-        __syncthreads();
-        if (w < 2) {
-            if (w == 1) G += *reinterpret_cast<double*>(sm + Lay::TOT);
-            const float hi = (float)G;
-            gh[i] = hi;
-            gl[i] = (float)(G - (double)hi);
-        }
-        __syncthreads();
+        // ---- row i of A, or of M.  Left of the warp's diagonal blocks of 16 the decay
+        // e^(Gamma_i - Gamma_j) = e^(Gamma_i - Gamma_r) e^(Gamma_r - Gamma_j): one
+        // exponential a row and block, both factors at most 1.
         const float ghi = gh[i], glo = gl[i];
-        if (w < 2) {
-            const float eg = ex2_approx(ghi);
-            vec[i] = -eg * rk[i];
-            vec[C + i] = eg * rq[i];
-            vec[2 * C + i] = ex2_approx((gh[C - 1] - ghi) + (gl[C - 1] - glo)) * rk[i];
-            if (i == C - 1) vec[3 * C] = eg;
-            if (i == 0) vec[3 * C + 1] = *reinterpret_cast<const float*>(sm + Lay::YS);
-        }
-        // ---- row i of A, or of M
         const float f = w < 2 ? be[i] * rk[i] : rq[i];
         const int edge = w < 2 ? i : i + 1;              // columns below it belong to the triangle
-#pragma unroll
+        const int diag = 32 * (w & 1);                   // the warp's rows are diag .. diag + 31
+#pragma unroll 1
         for (int j0 = 0; j0 < C; j0 += 16) {
             float x[16];
-            if (j0 <= ((w & 1) << 5) + 31) {             // warp-uniform: some row of the warp reaches these columns
+            if (j0 < diag + 32) {                        // warp-uniform
                 tmem_ld16(tbase + ((uint32_t)(32 * w) << 16) + j0, x);
+                if (j0 < diag) {
+                    const float u = ex2_approx((ghi - gh[j0 + 15]) + (glo - gl[j0 + 15])) * f;
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const int j = j0 + q;
-                    const float e = ex2_approx((ghi - gh[j]) + (glo - gl[j]));
-                    x[q] = j < edge ? x[q] * f * (e * rk[j]) : 0.f;
+                    for (int q = 0; q < 16; q += 4) {
+                        const float4 v4 = *reinterpret_cast<const float4*>(vj + j0 + q);
+                        x[q] *= u * v4.x; x[q + 1] *= u * v4.y; x[q + 2] *= u * v4.z; x[q + 3] *= u * v4.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4) {
+                        const float4 h4 = *reinterpret_cast<const float4*>(gh + j0 + q);
+                        const float4 l4 = *reinterpret_cast<const float4*>(gl + j0 + q);
+                        const float4 r4 = *reinterpret_cast<const float4*>(rk + j0 + q);
+                        const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
+                        const float rj[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float dec = ex2_approx((ghi - hj[e]) + (glo - lj[e]));
+                            x[q + e] = j0 + q + e < edge ? x[q + e] * f * (dec * rj[e]) : 0.f;
+                        }
+                    }
                 }
             } else {
 #pragma unroll
@@ -361,35 +426,29 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaChunkParams p) {
             }
         }
         __syncthreads();
-        // ---- T = (I + A)^-1 diag(beta): column j = tid, then its parts over A
-        float2 t[C / 2];
-        if (w < 2) delta_invert_column(A, Lay::LDA, tid, w == 0, t);
-        __syncthreads();
-        if (w < 2) {
-            const float bj = be[tid];
-            const int odd = lane & 1;
-#pragma unroll
-            for (int q = 0; q < C / 2; ++q) {            // rows 2q, 2q + 1: neighbouring lanes trade halves
-                uint32_t hi, lo;
-                split_f16(make_float2(t[q].x * bj, t[q].y * bj), hi, lo);
-                const uint32_t oh = __shfl_xor_sync(0xffffffffu, hi, 1), ol = __shfl_xor_sync(0xffffffffu, lo, 1);
-                const int row = 2 * q + odd;
-                const int off = row * 128 + ((((tid & ~1) >> 3) ^ (row & 7)) << 4) + (tid & 6) * 2;
-                *reinterpret_cast<uint32_t*>(sm + Lay::A + off) = odd ? __byte_perm(oh, hi, 0x7632) : __byte_perm(hi, oh, 0x5410);
-                *reinterpret_cast<uint32_t*>(sm + Lay::A + kDlTile + off) =
-                    odd ? __byte_perm(ol, lo, 0x7632) : __byte_perm(lo, ol, 0x5410);
-            }
+        delta_invert<Lay::LDA, Lay::LDW>(A, reinterpret_cast<float*>(sm + Lay::W), tid);
+        // ---- the blob: T = (I + A)^-1 diag(beta) as fp16 hi and lo tiles, M, the vectors
+        unsigned char* blob = p.blob + (((size_t)b * d.H + h) * p.nC + c) * kDlBlob;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            const int row = (tid >> 3) + 16 * k, pc = tid & 7;
+            const float4 a0 = *reinterpret_cast<const float4*>(A + row * Lay::LDA + 8 * pc);
+            const float4 a1 = *reinterpret_cast<const float4*>(A + row * Lay::LDA + 8 * pc + 4);
+            const float4 b0 = *reinterpret_cast<const float4*>(be + 8 * pc), b1 = *reinterpret_cast<const float4*>(be + 8 * pc + 4);
+            uint4 hi, lo;
+            split_f16(make_float2(a0.x * b0.x, a0.y * b0.y), hi.x, lo.x);
+            split_f16(make_float2(a0.z * b0.z, a0.w * b0.w), hi.y, lo.y);
+            split_f16(make_float2(a1.x * b1.x, a1.y * b1.y), hi.z, lo.z);
+            split_f16(make_float2(a1.z * b1.z, a1.w * b1.w), hi.w, lo.w);
+            const int off = row * 128 + ((pc ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(blob + off) = hi;
+            *reinterpret_cast<uint4*>(blob + kDlTile + off) = lo;
         }
-        __syncthreads();
-        // ---- the blob: T hi, T lo, M, vectors (16-byte pieces, coalesced)
-        uint4* blob = reinterpret_cast<uint4*>(p.blob + (((size_t)b * d.H + h) * p.nC + c) * kDlBlob);
-#pragma unroll
-        for (int k = 0; k < 2 * kDlTile / 16 / 128; ++k)
-            blob[tid + 128 * k] = *reinterpret_cast<const uint4*>(sm + Lay::A + (tid + 128 * k) * 16);
 #pragma unroll
         for (int k = 0; k < kDlTile / 16 / 128; ++k)
-            blob[2 * kDlTile / 16 + tid + 128 * k] = *reinterpret_cast<const uint4*>(sm + Lay::M + (tid + 128 * k) * 16);
-        if (tid < kDlVec / 16) blob[3 * kDlTile / 16 + tid] = *reinterpret_cast<const uint4*>(sm + Lay::V + tid * 16);
+            reinterpret_cast<uint4*>(blob + 2 * kDlTile)[tid + 128 * k] =
+                *reinterpret_cast<const uint4*>(sm + Lay::M + (tid + 128 * k) * 16);
+        if (tid < kDlVec / 16) reinterpret_cast<float4*>(blob + 3 * kDlTile)[tid] = reinterpret_cast<const float4*>(vec)[tid];
         __syncthreads();
     }
     tc_fence_before();
