@@ -444,10 +444,22 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * (B,G,N), v (B,H,P), rows ldq, ldk, ldv apart; dt_raw, b_raw (B,H); y
  * (B,H,P)), state (B,H,P,N) float32 updated in place.
  *
+ * bf16 sequences go in chunks of 64 tokens on the tensor cores: a prep launch
+ * makes each chunk's triangular factor and masked scores, and walks take the
+ * state from chunk to chunk.  With few heads the sequence is cut into
+ * `segments` runs of whole chunks (0: chosen for the current device; at most
+ * 64 and one per chunk): a first launch walks all but the last for their end
+ * states and transitions, and the walk of each segment enters with the fold of
+ * those before it.  float32 and very short sequences go token by token.
+ *
  * `workspace` (16-byte aligned; may be NULL when the size is 0) holds
- * axon_delta_workspace_bytes(B, L, H, G, P, N, io) bytes.  Every call writes
- * what it reads there, so calls that may run at the same time (streams,
- * captured graphs) need one each.  Pointers 16-byte aligned and ldq, ldk, ldv
+ * axon_delta_workspace_bytes(B, L, H, G, P, N, io, segments) bytes for the
+ * same `segments` on the current device.  Where it is used, its first 4 bytes
+ * (an int) are an error flag, cleared by each call and set to 1 if a wait of a
+ * kernel for its copies or products gave up (the outputs are then undefined);
+ * read it after the call completes.  Every call writes what it reads in the
+ * workspace, so calls that may run at the same time (streams, captured graphs)
+ * need one each.  Pointers 16-byte aligned and ldq, ldk, ldv
  * multiples of 8 (bf16) or 4 (f32), else AXON_ERR_ALIGNMENT; y, h_out and the
  * workspace overlap no input (but h_out may be h0) nor each other
  * (AXON_ERR_INVALID_ARG).  B, H <= 65535 and B*L*H <= 2^31, else
@@ -455,14 +467,14 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * zeros) to h_out.  Everything is float32 inside.  Other conventions as
  * above.
  */
-AXON_API size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io);
+AXON_API size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io, int segments);
 
 AXON_API axon_status axon_delta_scan_fwd(
     int B, int L, int H, int G, int P, int N, axon_dtype io,
     const void *q, int ldq, const void *k, int ldk, const void *v, int ldv,
     const void *dt_raw, const void *b_raw, const float *dt_bias, const float *A_log,
     const int *lengths, const float *h0, float scale, int qk_norm,
-    void *y, float *h_out, void *workspace, size_t workspace_bytes, axon_stream_t stream);
+    void *y, float *h_out, int segments, void *workspace, size_t workspace_bytes, axon_stream_t stream);
 
 AXON_API axon_status axon_delta_step(
     int B, int H, int G, int P, int N, axon_dtype io,

@@ -77,10 +77,10 @@ _lib.axon_ssd_workspace_bytes.argtypes = [_i] * 6
 _lib.axon_ssd_scan_fwd.restype = _i
 _lib.axon_ssd_scan_fwd.argtypes = [_i] * 6 + [_vp] * 10 + [_i, _vp, _sz, _vp]
 _lib.axon_delta_workspace_bytes.restype = _sz
-_lib.axon_delta_workspace_bytes.argtypes = [_i] * 7
+_lib.axon_delta_workspace_bytes.argtypes = [_i] * 8
 _lib.axon_delta_scan_fwd.restype = _i
 _lib.axon_delta_scan_fwd.argtypes = ([_i] * 7 + [_vp, _i] * 3 + [_vp] * 6 + [ctypes.c_float, _i] +
-                                     [_vp] * 3 + [_sz, _vp])
+                                     [_vp] * 2 + [_i, _vp, _sz, _vp])
 _lib.axon_delta_step.restype = _i
 _lib.axon_delta_step.argtypes = [_i] * 6 + [_vp, _i] * 3 + [_vp] * 4 + [ctypes.c_float, _i] + [_vp] * 3
 _lib.axon_gated_norm_fwd.restype = _i
@@ -304,8 +304,8 @@ def axon_ssd_scan_fwd(B, L, H, P, N, io, x, dt_raw, dt_bias, A_log, Bm, Cm, D, h
     return rc
 
 
-def axon_delta_workspace_bytes(B, L, H, G, P=128, N=128, io=AXON_BF16) -> int:
-    return int(_lib.axon_delta_workspace_bytes(B, L, H, G, P, N, io))
+def axon_delta_workspace_bytes(B, L, H, G, P=128, N=128, io=AXON_BF16, segments=0) -> int:
+    return int(_lib.axon_delta_workspace_bytes(B, L, H, G, P, N, io, segments))
 
 
 def _v(t):
@@ -314,11 +314,11 @@ def _v(t):
 
 
 def axon_delta_scan_fwd(B, L, H, G, P, N, io, q, ldq, k, ldk, v, ldv, dt_raw, b_raw, dt_bias, A_log, lengths, h0,
-                        scale, qk_norm, y, h_out, workspace, workspace_bytes, stream=None, *,
+                        scale, qk_norm, y, h_out, segments, workspace, workspace_bytes, stream=None, *,
                         raise_on_error=True) -> int:
     rc = _lib.axon_delta_scan_fwd(B, L, H, G, P, N, io, _v(q), ldq, _v(k), ldk, _v(v), ldv, _p(dt_raw), _p(b_raw),
                                   _p(dt_bias), _p(A_log), _p(lengths), _p(h0), scale, qk_norm, _p(y), _p(h_out),
-                                  _p(workspace), int(workspace_bytes), _stream(stream))
+                                  segments, _p(workspace), int(workspace_bytes), _stream(stream))
     if raise_on_error:
         _check(rc, "axon_delta_scan_fwd")
     return rc
@@ -683,7 +683,7 @@ def delta_error_flag(workspace) -> int:
 
 
 def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, scale=None, qk_norm=True, out=None,
-               workspace=None, stream=None, check=True):
+               workspace=None, stream=None, segments=0, check=True):
     """Gated delta rule prefill: q, k (B,L,G,N), v (B,L,H,P), dt_raw, b_raw
     (B,L,H); ``params`` holds dt_bias, A_log (H,) float32.  Returns
     ``(y (B,L,H,P), h_out (B,H,P,N))``, h_out ready for the next call or for
@@ -692,7 +692,8 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     q, k and v may be slices of one projected row (dense heads, tokens at one
     stride).  ``lengths`` ((B,) int32 on the device) ends rows early: y behind
     a row's end is left as it was (undefined where y is allocated here).
-    ``scale`` defaults to N^(-1/2).  ``out`` = (y, h_out); h_out may be h0.
+    ``scale`` defaults to N^(-1/2); ``segments`` = 0 lets the library cut the
+    sequence for the current device.  ``out`` = (y, h_out); h_out may be h0.
     With ``check`` the call waits for the device and raises AxonError
     (AXON_ERR_TIMEOUT) if a wait of the kernel gave up; ``check=False`` returns
     at once (read the flag with ``delta_error_flag(workspace)``).
@@ -703,7 +704,7 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return delta_scan(q, k, v, dt_raw, b_raw, params, h0, lengths=lengths, scale=scale, qk_norm=qk_norm,
-                              out=out, workspace=workspace, stream=stream, check=check)
+                              out=out, workspace=workspace, stream=stream, segments=segments, check=check)
     made = []
     if out is None:
         y = torch.empty(Bsz, L, H, P, dtype=v.dtype, device=dev)
@@ -715,13 +716,13 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     state = (Bsz, H, P, N)
     _like("delta_scan", torch.float32, h0=(h0, state), h_out=(h_out, state), y=(y, v.shape, v.dtype),
           lengths=(lengths, (Bsz,), torch.int32))
-    nbytes = axon_delta_workspace_bytes(Bsz, L, H, G, P, N, io)
+    nbytes = axon_delta_workspace_bytes(Bsz, L, H, G, P, N, io, segments)
     if workspace is None and nbytes > 0:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         made.append(workspace)
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    axon_delta_scan_fwd(Bsz, L, H, G, P, N, io, *args, lengths, h0, scale, int(qk_norm), y, h_out, workspace, wsz,
-                        stream=stream)
+    axon_delta_scan_fwd(Bsz, L, H, G, P, N, io, *args, lengths, h0, scale, int(qk_norm), y, h_out, segments, workspace,
+                        wsz, stream=stream)
     _used_on(stream, dev, *made)
     if check and nbytes > 0 and delta_error_flag(workspace) != 0:
         raise AxonError(6, "axon_delta_scan_fwd (a wait for a copy or a tensor-core product gave up)")

@@ -93,19 +93,57 @@ void launch_recur(const DeltaParams& p, cudaStream_t st) {
 
 // bf16 sequences of at least this many tokens go in chunks.
 constexpr int kChunkedFrom = 32;
+constexpr int kDlMaxSegs = 64;
 bool chunked(int L, axon_dtype io) { return io == AXON_BF16 && L >= kChunkedFrom; }
 
-struct DeltaWs {
-    size_t err, kq, blob, total;
-};
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-DeltaWs delta_ws(int B, int L, int H, int G, int N) {
-    const size_t nC = ((size_t)L + kDlC - 1) / kDlC;
+
+// Segments of whole chunks.  One walk runs on an SM at a time, so a pass takes
+// ceil(walks / SMs) rounds of one segment's chunks; a chunk of the pass
+// without outputs costs about 2/3 of one with them, a fold about half a chunk,
+// and the second launch about two.  `requested` > 0 asks for that many.
+struct DeltaPlan {
+    int segs, cps;
+};
+DeltaPlan delta_plan(int B, int L, int H, int requested) {
+    const int nC = (L + kDlC - 1) / kDlC;
+    const int most = std::min(nC, kDlMaxSegs);
+    auto cut = [&](int segs) {
+        const int cps = (nC + segs - 1) / segs;
+        return DeltaPlan{(nC + cps - 1) / cps, cps};
+    };
+    if (nC <= 1) return DeltaPlan{1, std::max(nC, 1)};
+    if (requested > 0) return cut(std::min(requested, most));
+    const long long sms = sm_count(), walks = (long long)B * H;
+    DeltaPlan best{1, nC};
+    double least = 1e300;
+    for (int want = 1; want <= most; ++want) {
+        const DeltaPlan p = cut(want);
+        const long long full = (p.segs * walks + sms - 1) / sms, state = ((2 * p.segs - 3) * walks + sms - 1) / sms;
+        const double t = full * p.cps + (p.segs > 1 ? 0.67 * state * p.cps + 0.5 * (p.segs - 2) + 2.0 : 0.0);
+        if (t < least) {
+            least = t;
+            best = p;
+        }
+    }
+    return best;
+}
+
+struct DeltaWs {
+    size_t err, kq, blob, sloc, tr, trs, h0c, total;
+};
+DeltaWs delta_ws(int B, int L, int H, int G, int P, int N, const DeltaPlan& plan) {
+    const size_t nC = ((size_t)L + kDlC - 1) / kDlC, BH = (size_t)B * H;
+    const size_t loc = plan.segs > 1 ? plan.segs - 1 : 0, tr = plan.segs > 2 ? plan.segs - 2 : 0;
     DeltaWs w{};
     w.err = 0;
     w.kq = 256;
     w.blob = w.kq + (size_t)B * G * nC * 128 * N * 2;
-    w.total = w.blob + up256((size_t)B * H * nC * kDlBlob);
+    w.sloc = w.blob + up256(BH * nC * kDlBlob);
+    w.tr = w.sloc + loc * BH * P * N * 4;
+    w.trs = w.tr + tr * BH * 2 * N * N * 2;
+    w.h0c = w.trs + up256(tr * BH * N * 4);
+    w.total = w.h0c + (plan.segs > 1 ? BH * P * N * 4 : 0);
     return w;
 }
 
@@ -134,27 +172,33 @@ bool v_map(CUtensorMap* m, const DeltaParams& d) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int N, int P>
-axon_status launch_chunked(const DeltaChunkParams& p, cudaStream_t st) {
-    static std::atomic<unsigned long long> prep_ok{0}, walk_ok{0};
-    if (!allow_smem(delta_prep_kernel<N>, DeltaPrepSmem<N>::TOTAL, prep_ok) ||
-        !allow_smem(delta_walk_kernel<N, P>, DeltaWalkSmem<N, P>::TOTAL, walk_ok))
-        return AXON_ERR_CUDA;
-    CUtensorMap tmV;
-    if (!v_map(&tmV, p.d)) return AXON_ERR_CUDA;
-    delta_prep_kernel<N><<<dim3((unsigned)p.nC, (unsigned)p.d.G, (unsigned)p.d.B), 128, DeltaPrepSmem<N>::TOTAL, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return AXON_ERR_CUDA;
+template <int N, int P, bool kFull>
+bool launch_walk(const CUtensorMap& tmV, const DeltaChunkParams& p, cudaStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    constexpr int smem = DeltaWalkSmem<N, P>::TOTAL;
+    if (!allow_smem(delta_walk_kernel<N, P, kFull>, smem, done)) return false;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)p.d.H, (unsigned)p.d.B, 1);
+    c.gridDim = dim3((unsigned)p.d.H, (unsigned)p.d.B, (unsigned)(kFull ? p.segs : 2 * p.segs - 3));
     c.blockDim = dim3(kDlThreads, 1, 1);
-    c.dynamicSmemBytes = DeltaWalkSmem<N, P>::TOTAL;
+    c.dynamicSmemBytes = smem;
     c.stream = st;
     c.attrs = pdl;
     c.numAttrs = 1;
-    if (cudaLaunchKernelEx(&c, delta_walk_kernel<N, P>, tmV, p) != cudaSuccess) return AXON_ERR_CUDA;
+    return cudaLaunchKernelEx(&c, delta_walk_kernel<N, P, kFull>, tmV, p) == cudaSuccess;
+}
+template <int N, int P>
+axon_status launch_chunked(const DeltaChunkParams& p, cudaStream_t st) {
+    static std::atomic<unsigned long long> prep_ok{0};
+    if (!allow_smem(delta_prep_kernel<N>, DeltaPrepSmem<N>::TOTAL, prep_ok)) return AXON_ERR_CUDA;
+    CUtensorMap tmV;
+    if (!v_map(&tmV, p.d)) return AXON_ERR_CUDA;
+    delta_prep_kernel<N><<<dim3((unsigned)p.nC, (unsigned)p.d.G, (unsigned)p.d.B), 128, DeltaPrepSmem<N>::TOTAL, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return AXON_ERR_CUDA;
+    if (p.segs > 1 && !launch_walk<N, P, false>(tmV, p, st)) return AXON_ERR_CUDA;
+    if (!launch_walk<N, P, true>(tmV, p, st)) return AXON_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? AXON_OK : AXON_ERR_CUDA;
 }
 
@@ -185,18 +229,18 @@ using namespace axon;
 
 extern "C" {
 
-size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io) {
-    if (B <= 0 || L < 0 || H <= 0 || !shape_ok(H, G, P, N) || !chunked(L, io)) return 0;
-    return delta_ws(B, L, H, G, N).total;
+size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io, int segments) {
+    if (B <= 0 || L < 0 || H <= 0 || segments < 0 || !shape_ok(H, G, P, N) || !chunked(L, io)) return 0;
+    return delta_ws(B, L, H, G, P, N, delta_plan(B, L, H, segments)).total;
 }
 
 axon_status axon_delta_scan_fwd(int B, int L, int H, int G, int P, int N, axon_dtype io,
                                 const void* q, int ldq, const void* k, int ldk, const void* v, int ldv,
                                 const void* dt_raw, const void* b_raw, const float* dt_bias, const float* A_log,
                                 const int* lengths, const float* h0, float scale, int qk_norm,
-                                void* y, float* h_out, void* workspace, size_t workspace_bytes,
+                                void* y, float* h_out, int segments, void* workspace, size_t workspace_bytes,
                                 axon_stream_t stream) {
-    if (B < 0 || L < 0 || H < 0) return AXON_ERR_INVALID_ARG;
+    if (B < 0 || L < 0 || H < 0 || segments < 0) return AXON_ERR_INVALID_ARG;
     if (B > 65535 || H > 65535 || (long long)B * L * H > (1LL << 31)) return AXON_ERR_UNSUPPORTED;
     if (B == 0 || H == 0) return AXON_OK;
     const size_t rows = (size_t)B * L;
@@ -205,7 +249,9 @@ axon_status axon_delta_scan_fwd(int B, int L, int H, int G, int P, int N, axon_d
     if (!h_out || (rows > 0 && !y)) return AXON_ERR_INVALID_ARG;
     if (!al16(y) || !al16(h_out) || !al16(h0) || !al16(workspace) || (reinterpret_cast<uintptr_t>(lengths) & 3u))
         return AXON_ERR_ALIGNMENT;
-    const size_t n_ws = axon_delta_workspace_bytes(B, L, H, G, P, N, io);
+    const DeltaPlan plan = delta_plan(B, L, H, segments);
+    const DeltaWs w = delta_ws(B, L, H, G, P, N, plan);
+    const size_t n_ws = chunked(L, io) ? w.total : 0;
     if (workspace_bytes < n_ws) return AXON_ERR_WORKSPACE;
     if (n_ws > 0 && !workspace) return AXON_ERR_INVALID_ARG;
     const size_t es = io == AXON_BF16 ? 2 : 4;
@@ -224,9 +270,11 @@ axon_status axon_delta_scan_fwd(int B, int L, int H, int G, int P, int N, axon_d
     DeltaParams p{B, L, H, G, P, ldq, ldk, ldv, q, k, v, dt_raw, b_raw, dt_bias, A_log, lengths, h0, y, h_out, scale, qk_norm != 0};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (chunked(L, io)) {
-        const DeltaWs w = delta_ws(B, L, H, G, N);
         unsigned char* ws = static_cast<unsigned char*>(workspace);
-        const DeltaChunkParams c{p, (L + kDlC - 1) / kDlC, ws + w.kq, ws + w.blob, reinterpret_cast<int*>(ws + w.err)};
+        const bool split = plan.segs > 1;
+        const DeltaChunkParams c{p, (L + kDlC - 1) / kDlC, ws + w.kq, ws + w.blob, reinterpret_cast<int*>(ws + w.err),
+                                 plan.segs, plan.cps, reinterpret_cast<float*>(ws + w.sloc), ws + w.tr,
+                                 reinterpret_cast<float*>(ws + w.trs), split && h0 ? reinterpret_cast<float*>(ws + w.h0c) : nullptr};
         if (N == 128) return P == 128 ? launch_chunked<128, 128>(c, st) : launch_chunked<128, 64>(c, st);
         return P == 128 ? launch_chunked<64, 128>(c, st) : launch_chunked<64, 64>(c, st);
     }

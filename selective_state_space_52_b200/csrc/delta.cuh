@@ -26,6 +26,13 @@
 // its part of R is there: the conversions of one half run beside the products
 // of the other.
 //
+// A walk takes the chunks of one head one after the other, so few heads leave
+// most SMs idle.  Then the sequence is cut into segments: a first pass walks
+// every segment but the last without outputs, once from a zero state (its end
+// state) and once from the identity without V (its transition, N x N; the
+// delta rule's is a full matrix, not a decay), and the walk of segment s enters
+// with S_(j+1) = S_j M_j + S_loc,j folded over the segments before it.
+//
 // Precision.  Operands are fp16 with float32 accumulators.  K and Q enter
 // scaled by a power of two per token (largest element in [1/2, 1)): exact, but
 // for bits below 2^-25 of the row.  S, R, U (for the state) and T enter as two
@@ -61,6 +68,12 @@ struct DeltaChunkParams {
     unsigned char* kq;           // (B, G, nC): K', then Q': fp16, 64 rows in 64-column blocks, 128-byte swizzle
     unsigned char* blob;         // (B, H, nC): kDlBlob bytes
     int* err;                    // set to 1 when a wait gave up
+    // the sequence in segments of cps chunks, when there are few heads:
+    int segs, cps;
+    float* sloc;                 // (segs - 1, B, H, P, N): a segment's end state from zeros (the first: from h0)
+    unsigned char* tr;           // (segs - 2, B, H): transitions of segments 1 .., fp16 hi and lo tiles (N x N)
+    float* trs;                  // (segs - 2, B, H, N): what a transition's row is in units of
+    float* h0c;                  // (B, H, P, N): h0 again (h_out may lie over it)
 };
 
 // kind::f16 instruction descriptor with fp16 A and B, float32 D
@@ -183,6 +196,7 @@ __device__ __forceinline__ void delta_invert(float* A, float* W, int tid) {
     __syncthreads();
     {
         const int r = tid >> 2, c = (tid & 3) * 8;
+        const int kend = (r & ~7) + 8;                   // T22 is 0 behind its diagonal (warp-uniform)
         float* row = A + (32 + r) * LDA;
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {           // W = A21 T11, then T21 = -T22 W
@@ -191,7 +205,7 @@ __device__ __forceinline__ void delta_invert(float* A, float* W, int tid) {
             const float* y = pass ? W + c : A + c;
             const int ldy = pass ? LDW : LDA;
 #pragma unroll 4
-            for (int k = 0; k < 32; ++k) {
+            for (int k = 0; k < (pass ? kend : 32); ++k) {
                 const float xv = x[k];
                 const float4 y0 = *reinterpret_cast<const float4*>(y + k * ldy), y1 = *reinterpret_cast<const float4*>(y + k * ldy + 4);
                 s[0] = fmaf(xv, y0.x, s[0]); s[1] = fmaf(xv, y0.y, s[1]); s[2] = fmaf(xv, y0.z, s[2]); s[3] = fmaf(xv, y0.w, s[3]);
@@ -457,7 +471,8 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
     if (w == 0 && !failed) tmem_dealloc(tbase, 64);      // after a failed wait a late product might still write
 }
 
-// ---- the walk: grid = (H, B), 576 threads.  Warps 0 .. 15 compute: warp w holds
+// ---- the walk: grid = (H, B, segments), 576 threads; without outputs grid =
+// (H, B, 2 segments - 3): end states of segments 0 .., then transitions of 1 ...  Warps 0 .. 15 compute: warp w holds
 // lanes 32 (w & 3) .. of tensor memory, and the four warps of such a quadrant
 // share its lanes' work, thread `part` = w >> 2 of a lane taking a quarter of
 // the state row and of the tokens.  (One warp a quadrant, two blocks an SM,
@@ -483,11 +498,13 @@ struct DeltaWalkSmem {
     static constexpr int SMAX = VM + kDlStages * P * 4;   // largest |S| of the quarters of a lane's state row
     static constexpr int MB = SMAX + 4 * 128 * 4;
     enum { FULL, VMAX = FULL + kDlStages, X_K0 = VMAX + kDlStages, X_K1, X_Q, U_0, U_1, Y_M, D, S_IN, R_IN0, R_IN1, U_IN0,
-           U_IN1, Y_OUT, QUAD, DRAIN = QUAD + 4, BARS };
+           U_IN1, Y_OUT, QUAD, DRAIN = QUAD + 4, TR_FULL, BARS = TR_FULL + 2 };
     static constexpr int DEAD = MB + 8 * BARS;            // a wait gave up
     static constexpr int SLOT = DEAD + 4;
     static constexpr int BYTES = SLOT + 4;
     static constexpr int TOTAL = BYTES + 1024;
+    static constexpr int TR_BYTES = N * N * 2;            // a part of a transition, in the stages after the first
+    static_assert(2 * TR_BYTES <= STAGE, "a transition fits a stage");
     static_assert(TOTAL <= 227 * 1024, "shared memory of a block");
     static_assert(STAGE % 1024 == 0 && VEC % 128 == 0, "swizzled tiles and copies aligned");
     // tensor memory: the A operands hold two fp16 a column; 16 tokens of R and U_w are 8 columns hi, 8 lo
@@ -523,7 +540,7 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
 }
 
-template <int N, int P>
+template <int N, int P, bool kFull>
 __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_constant__ CUtensorMap tmV, DeltaChunkParams p) {
     using Lay = DeltaWalkSmem<N, P>;
     constexpr int C = kDlC, KS = N / 16, ST = kDlStages;
@@ -537,14 +554,20 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
     const DeltaParams& d = p.d;
     int len = d.L;
     if (d.lengths) len = min(max(__ldg(d.lengths + b), 0), d.L);
-    const int nC = (len + C - 1) / C;
+    // this block's chunks: cb .. cb + nC - 1
+    const bool trans = !kFull && (int)blockIdx.z >= p.segs - 1;
+    const int seg = trans ? blockIdx.z - (p.segs - 1) + 1 : blockIdx.z;
+    const int all = (len + C - 1) / C, cb = seg * p.cps, nC = min(p.cps, all - cb);
+    if (nC <= 0 && seg > 0) return;                       // whole block; an empty row's state passes through segment 0
+    const int nf = kFull && seg > 1 ? seg - 1 : 0;        // transitions to fold into the entering state
+    const int lanes = trans ? N : P;
     const int g = h / (d.H / d.G);
     volatile int* dead = reinterpret_cast<volatile int*>(sm + Lay::DEAD);
     auto bar = [&](int i) { return sb + Lay::MB + 8 * i; };
 
     if (tid == 0) {
         for (int i = 0; i < Lay::BARS; ++i)
-            mbar_init(bar(i), i >= Lay::S_IN && i <= Lay::Y_OUT ? P / 8 : i >= Lay::QUAD && i < Lay::DRAIN ? 4 : 1);   // warps
+            mbar_init(bar(i), i >= Lay::S_IN && i <= Lay::Y_OUT ? lanes / 8 : i >= Lay::QUAD && i < Lay::DRAIN ? 4 : 1);   // warps
         *dead = 0;
         fence_mbar_init();
     }
@@ -561,20 +584,30 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
         // ---------------- copies and products.  The warp runs the loop together and one
         // lane issues: in a region of one lane only, addresses live in vector
         // registers, and a product costs twice what the tensor core takes for it.
-        const unsigned char* kq = p.kq + ((size_t)b * d.G + g) * p.nC * (2 * Lay::K_BYTES);
-        const unsigned char* blob = p.blob + ((size_t)b * d.H + h) * p.nC * kDlBlob;
+        const unsigned char* kq = p.kq + (((size_t)b * d.G + g) * p.nC + cb) * (2 * Lay::K_BYTES);
+        const unsigned char* blob = p.blob + (((size_t)b * d.H + h) * p.nC + cb) * kDlBlob;
+        const uint32_t v_bytes = trans ? 0 : Lay::V_BYTES;
         auto load_chunk = [&](int c, int st) {            // V's rows past L read as zeros
             if (elect_one()) {
                 const uint32_t full = bar(Lay::FULL + st), dst = sb + st * Lay::STAGE;
-                mbar_arrive_expect_tx(full, Lay::STAGE);
-                bulk_load(dst + Lay::K, kq + (size_t)c * 2 * Lay::K_BYTES, 2 * Lay::K_BYTES, full);
-                tma_load_3d(dst + Lay::V, &tmV, h * P, c * C, b, full);
-                bulk_load(dst + Lay::T, blob + (size_t)c * kDlBlob, kDlBlob, full);
+                mbar_arrive_expect_tx(full, (kFull ? 2 * Lay::K_BYTES + kDlBlob : Lay::K_BYTES + 2 * kDlTile + kDlVec) + v_bytes);
+                const unsigned char* src = blob + (size_t)c * kDlBlob;
+                bulk_load(dst + Lay::K, kq + (size_t)c * 2 * Lay::K_BYTES, (kFull ? 2 : 1) * Lay::K_BYTES, full);
+                if (!trans) tma_load_3d(dst + Lay::V, &tmV, h * P, (cb + c) * C, b, full);
+                if constexpr (kFull) {
+                    bulk_load(dst + Lay::T, src, kDlBlob, full);
+                } else {
+                    bulk_load(dst + Lay::T, src, 2 * kDlTile, full);
+                    bulk_load(dst + Lay::VEC, src + 3 * kDlTile, kDlVec, full);
+                }
             }
         };
         static_assert(Lay::V - Lay::T == kDlBlob, "T, M and the vectors lie as in the blob");
         int loaded = 0;
-        for (; loaded < min(nC, ST); ++loaded) load_chunk(loaded, loaded);
+        if (nf == 0)
+            for (; loaded < min(nC, ST); ++loaded) load_chunk(loaded, loaded);
+        else if (nC > 0)
+            load_chunk(loaded++, 0);                      // the other stages hold the transitions first
         constexpr uint32_t kId64 = umma_idesc_f16(128, 64, 0, 0);    // B K-major: K', Q', T, M rows
         constexpr uint32_t kId32 = umma_idesc_f16(128, 32, 0, 0);
         constexpr uint32_t kIdS = umma_idesc_f16(128, N, 0, 1);      // B: K' rows as the K dimension (MN-major)
@@ -585,9 +618,40 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
         auto rows = [](int ks) { return (ks >> 2) * 8192 + (ks & 3) * 32; };     // K step ks of a 64-row tile
         const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
         bool ok = true;
-        for (int c = 0, st = 0, use = 0; c < nC; ++c) {
+        int folds = 0;                                    // transitions loaded
+        if constexpr (kFull) {
+            constexpr uint32_t kIdT = umma_idesc_f16(128, N, 0, 1);
+            const unsigned char* tr = p.tr + ((size_t)b * d.H + h) * 2 * Lay::TR_BYTES;
+            const size_t step = (size_t)d.B * d.H * 2 * Lay::TR_BYTES;
+            auto load_tr = [&](int j) {
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar(Lay::TR_FULL + (j & 1)), 2 * Lay::TR_BYTES);
+                    bulk_load(sb + (1 + (j & 1)) * Lay::STAGE, tr + j * step, 2 * Lay::TR_BYTES, bar(Lay::TR_FULL + (j & 1)));
+                }
+            };
+            if (nf > 0) { load_tr(0); folds = 1; }
+            for (int j = 0; j < nf; ++j) {                // S M: hi hi, lo hi, hi lo
+                if (!(ok = delta_wait(bar(Lay::TR_FULL + (j & 1)), j >> 1, dead) && delta_wait(bar(Lay::S_IN), j, dead))) break;
+                tc_fence_after();
+                if (j + 1 < nf) { load_tr(j + 1); ++folds; }      // the product that read that stage is done
+                const uint64_t t_d = umma_desc(sb + (1 + (j & 1)) * Lay::STAGE, N * 128, 1024);
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 3 * KS; ++ks)
+                        umma_ts(tb + Lay::XK, tb + (ks / KS == 1 ? Lay::S_LO : Lay::S_HI) + 8 * (ks % KS),
+                                at(t_d, (ks / KS == 2 ? Lay::TR_BYTES : 0) + (ks % KS) * 2048), kIdT, ks > 0);
+                    umma_commit(bar(Lay::D));
+                }
+            }
+            if (nf > 0 && ok) {
+                ok = delta_wait(bar(Lay::D), nf - 1, dead);
+                if (ok)
+                    for (; loaded < min(nC, ST); ++loaded) load_chunk(loaded, loaded);
+            }
+        }
+        for (int c = 0, st = 0, use = 0; c < nC && ok; ++c) {
             const uint64_t k_d = d_k + (uint64_t)(st * (Lay::STAGE >> 4)), ks_d = d_ks + (uint64_t)(st * (Lay::STAGE >> 4));
-            if (!(ok = delta_wait(bar(Lay::FULL + st), use, dead) && delta_wait(bar(Lay::S_IN), c, dead))) break;
+            if (!(ok = delta_wait(bar(Lay::FULL + st), use, dead) && delta_wait(bar(Lay::S_IN), nf + c, dead))) break;
             tc_fence_after();
             if (elect_one()) {                            // K S^T, both parts of S, 32 tokens at a time
 #pragma unroll
@@ -599,13 +663,15 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                     umma_commit(bar(Lay::X_K0 + half));
                 }
             }
-            if (!(ok = c == 0 || delta_wait(bar(Lay::Y_OUT), c - 1, dead))) break;
-            tc_fence_after();
-            if (elect_one()) {                            // Q S^T, the hi part
+            if constexpr (kFull) {
+                if (!(ok = c == 0 || delta_wait(bar(Lay::Y_OUT), c - 1, dead))) break;
+                tc_fence_after();
+                if (elect_one()) {                            // Q S^T, the hi part
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    umma_ts(tb + Lay::XQ, tb + Lay::S_HI + 8 * ks, at(k_d, Lay::Q + rows(ks)), kId64, ks > 0);
-                umma_commit(bar(Lay::X_Q));
+                    for (int ks = 0; ks < KS; ++ks)
+                        umma_ts(tb + Lay::XQ, tb + Lay::S_HI + 8 * ks, at(k_d, Lay::Q + rows(ks)), kId64, ks > 0);
+                    umma_commit(bar(Lay::X_Q));
+                }
             }
             // chunk c - 1 is done with its stage: its increment and its Y have been read
             if (c > 0 && loaded < nC) {
@@ -635,7 +701,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 umma_commit(bar(Lay::U_1));
             }
             // the increment goes where S is: Q S^T has to be done with it
-            if (!(ok = delta_wait(bar(Lay::X_Q), c, dead) && delta_wait(bar(Lay::U_IN0), c, dead))) break;
+            if (!(ok = (!kFull || delta_wait(bar(Lay::X_Q), c, dead)) && delta_wait(bar(Lay::U_IN0), c, dead))) break;
             tc_fence_after();
             auto increment = [&](int half) {              // U_w^T K, 16 tokens a step, hi and lo
 #pragma unroll
@@ -648,11 +714,13 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             if (elect_one()) {
                 increment(1);
                 umma_commit(bar(Lay::D));
+                if constexpr (kFull) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)            // Y += M U
-                    umma_ts(tb + Lay::XQ + (ks >> 1) * 32, tb + Lay::UH + 8 * ks, at(k_d, Lay::M + (ks >> 1) * 4096 + ks * 32),
-                            ks < 2 ? kId64 : kId32, 1);
-                umma_commit(bar(Lay::Y_M));
+                    for (int ks = 0; ks < 4; ++ks)        // Y += M U
+                        umma_ts(tb + Lay::XQ + (ks >> 1) * 32, tb + Lay::UH + 8 * ks, at(k_d, Lay::M + (ks >> 1) * 4096 + ks * 32),
+                                ks < 2 ? kId64 : kId32, 1);
+                    umma_commit(bar(Lay::Y_M));
+                }
             }
             if (++st == ST) { st = 0; ++use; }
         }
@@ -665,15 +733,16 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             __syncwarp();
             mbar_wait(bar(Lay::DRAIN), 0u);
             for (int i = max(0, loaded - ST); i < loaded; ++i) mbar_wait(bar(Lay::FULL + i % ST), (uint32_t)(i / ST) & 1);
+            for (int i = max(0, folds - 2); i < folds; ++i) mbar_wait(bar(Lay::TR_FULL + (i & 1)), (uint32_t)(i >> 1) & 1);
         }
         __syncwarp();
     } else if (w == 17) {
         // ---------------- the largest |v| of each column (bf16 bits order like their values)
         constexpr int PW = P / 64;                        // words (column pairs) a lane
-        for (int c = 0, st = 0, use = 0; c < nC; ++c) {
+        for (int c = 0, st = 0, use = 0; c < nC && !trans; ++c) {
             if (!delta_wait(bar(Lay::FULL + st), use, dead)) break;
             const uint32_t* v = reinterpret_cast<const uint32_t*>(sm + st * Lay::STAGE + Lay::V) + lane * PW;
-            const int rows = min(C, len - c * C);
+            const int rows = min(C, len - (cb + c) * C);
             uint32_t m[PW];
 #pragma unroll
             for (int i = 0; i < PW; ++i) m[i] = 0;
@@ -688,7 +757,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             if (lane == 0) mbar_arrive(bar(Lay::VMAX + st));
             if (++st == ST) { st = 0; ++use; }
         }
-    } else if ((w & 3) < P / 32) {
+    } else if ((w & 3) < lanes / 32) {
         // ---------------- four threads a value column
         const int part = w >> 2, v = 32 * (w & 3) + lane;
         constexpr int NQ = N / 4;                         // states of a thread: n = NQ part ..
@@ -696,11 +765,18 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
         float2 S[NQ / 2];                                 // lambda times its part of the state row
         float lam = 1.f, ilam = 1.f;                      // the lane's scale and its inverse
         const size_t hoff = (((size_t)b * d.H + h) * P + v) * N + NQ * part;
+        const size_t hstep = (size_t)d.B * d.H * P * N;   // floats between segments in sloc
+        const float* from = seg == 0 ? (kFull && p.h0c ? p.h0c : d.h0) : kFull ? p.sloc : nullptr;
 #pragma unroll
         for (int n = 0; n < NQ; n += 4) {
-            const float4 x = d.h0 ? *reinterpret_cast<const float4*>(d.h0 + hoff + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 x = from ? *reinterpret_cast<const float4*>(from + hoff + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!kFull && trans) {                        // the identity
+                const int e = v - NQ * part - n;
+                x = make_float4(e == 0, e == 1, e == 2, e == 3);
+            }
             S[n / 2] = make_float2(x.x, x.y);
             S[n / 2 + 1] = make_float2(x.z, x.w);
+            if (!kFull && seg == 0 && p.h0c) *reinterpret_cast<float4*>(p.h0c + hoff + n) = x;
         }
         float* smax = reinterpret_cast<float*>(sm + Lay::SMAX) + v;
         auto arrive = [&](int i) {
@@ -708,25 +784,83 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(i));
         };
+        // the largest |x| over the lane's four threads: told, then, once all have, read
+        auto lane_max = [&](const float2 (&x)[NQ / 2], float& m) {
+            m = 0.f;
+#pragma unroll
+            for (int n = 0; n < NQ / 2; ++n) m = max_abs3(m, x[n].x, x[n].y);
+            smax[128 * part] = m;
+            arrive(Lay::QUAD + (w & 3));
+        };
+        auto lane_max_wait = [&](int use, float& m) {
+            if (!delta_wait(bar(Lay::QUAD + (w & 3)), use, dead)) return false;
+            m = fmaxf(fmaxf(smax[0], smax[128]), fmaxf(smax[256], smax[384]));
+            return true;
+        };
         bool ok = true;
+        if constexpr (kFull) {
+            // ---- the state entering this segment: S M_j + S_loc,j over the segments before it
+            const float* trs = p.trs + ((size_t)b * d.H + h) * N + NQ * part;
+            for (int j = 0; j < nf; ++j) {
+                float m;
+#pragma unroll
+                for (int n = 0; n < NQ; n += 4) {         // to units in which M_j's rows are kept
+                    const float4 x = *reinterpret_cast<const float4*>(trs + (size_t)j * d.B * d.H * N + n);
+                    S[n / 2] = __fmul2_rn(S[n / 2], make_float2(x.x, x.y));
+                    S[n / 2 + 1] = __fmul2_rn(S[n / 2 + 1], make_float2(x.z, x.w));
+                }
+                lane_max(S, m);
+                if (!(ok = lane_max_wait(j, m))) break;
+                const int e = m > 0.f ? exp_above(m) : 0;
+                const float f = pow2i(-e), back = pow2i(e);
+#pragma unroll
+                for (int n0 = 0; n0 < NQ / 2; n0 += 8) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) split_f16(__fmul2_rn(S[n0 + q], make_float2(f, f)), hi[q], lo[q]);
+                    tmem_st8(tl + Lay::S_HI + NQ / 2 * part + n0, hi);
+                    tmem_st8(tl + Lay::S_LO + NQ / 2 * part + n0, lo);
+                }
+                tmem_st_wait();
+                arrive(Lay::S_IN);
+                const float* loc = p.sloc + (size_t)(j + 1) * hstep + hoff;
+#pragma unroll
+                for (int n = 0; n < NQ; n += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(loc + n);
+                    S[n / 2] = make_float2(x.x, x.y);
+                    S[n / 2 + 1] = make_float2(x.z, x.w);
+                }
+                if (!(ok = delta_wait(bar(Lay::D), j, dead))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int n0 = 0; n0 < NQ; n0 += 16) {
+                    float x[16];
+                    tmem_ld16(tl + Lay::XK + NQ * part + n0, x);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        S[n0 / 2 + q] = __ffma2_rn(make_float2(back, back), make_float2(x[2 * q], x[2 * q + 1]), S[n0 / 2 + q]);
+                }
+            }
+        }
         float yl = 0.f;                                   // what Y of the chunk before is in units of
-        for (int c = 0, st = 0, use = 0; c <= nC; ++c) {
+        for (int c = 0, st = 0, use = 0; c <= nC && ok; ++c) {
             const unsigned char* sg = sm + st * Lay::STAGE;
-            if (c < nC) {
+            if (c < nC || trans) {
                 // ---- the lane's scale for this chunk, S into the A operand's columns:
                 // first in the scale it has, which nearly always stands
-                float m = 0.f;
-#pragma unroll
-                for (int n = 0; n < NQ / 2; ++n) m = max_abs3(m, S[n].x, S[n].y);
-                smax[128 * part] = m;
-                arrive(Lay::QUAD + (w & 3));
+                float m;
+                lane_max(S, m);
                 uint32_t hi[NQ / 2], lo[NQ / 2];
 #pragma unroll
                 for (int q = 0; q < NQ / 2; ++q) split_f16(S[q], hi[q], lo[q]);
-                // every thread of the lane has told its largest and read its increment; V and the vectors are here
-                if (!(ok = delta_wait(bar(Lay::QUAD + (w & 3)), c, dead) && delta_wait(bar(Lay::VMAX + st), use, dead))) break;
-                m = fmaxf(fmaxf(smax[0], smax[128]), fmaxf(smax[256], smax[384]));
-                m = fmaxf(m, lam * reinterpret_cast<const float*>(sm + Lay::VM)[st * P + v]);
+                // every thread of the lane has read its increment too; V and the vectors are here
+                if (!(ok = lane_max_wait(nf + c, m))) break;
+                if (trans) {
+                    if (c < nC && !(ok = delta_wait(bar(Lay::FULL + st), use, dead))) break;
+                } else {
+                    if (!(ok = delta_wait(bar(Lay::VMAX + st), use, dead))) break;
+                    m = fmaxf(m, lam * reinterpret_cast<const float*>(sm + Lay::VM)[st * P + v]);
+                }
                 const bool out = m > 64.f || (m < 0.125f && m > 0.f);
                 if (__any_sync(0xffffffffu, out)) {
                     const int e = out ? exp_above(m) : 0;
@@ -740,6 +874,19 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                         split_f16(S[q], hi[q], lo[q]);
                     }
                 }
+                if (!kFull && c == nC) {                  // the segment's transition: row v, this thread's columns
+                    const size_t at = ((size_t)(seg - 1) * d.B + b) * d.H + h;
+                    unsigned char* tile = p.tr + at * 2 * Lay::TR_BYTES + (NQ * part / 64) * (N * 128) + v * 128;
+#pragma unroll
+                    for (int q = 0; q < NQ / 8; ++q) {
+                        const int off = (((NQ * part / 8 + q) & 7) ^ (v & 7)) << 4;
+                        *reinterpret_cast<uint4*>(tile + off) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+                        *reinterpret_cast<uint4*>(tile + Lay::TR_BYTES + off) =
+                            make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+                    }
+                    if (part == 0) p.trs[at * N + v] = ilam;
+                    break;
+                }
 #pragma unroll
                 for (int n0 = 0; n0 < NQ / 2; n0 += 8) {
                     tmem_st8(tl + Lay::S_HI + NQ / 2 * part + n0, reinterpret_cast<uint32_t(&)[8]>(hi[n0]));
@@ -750,10 +897,10 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             }
             // ---- y of chunk c - 1, while K S^T runs: 16 tokens a thread; neighbouring
             // lanes trade tokens, so a lane stores two columns of one token
-            if (c > 0) {
+            if (kFull && c > 0) {
                 if (!(ok = delta_wait(bar(Lay::Y_M), c - 1, dead))) break;
                 tc_fence_after();
-                const int odd = lane & 1, t0 = (c - 1) * C + 16 * part + odd, left = len - t0;
+                const int odd = lane & 1, t0 = (cb + c - 1) * C + 16 * part + odd, left = len - t0;
                 const size_t ystep = 2 * (size_t)d.H * P;
                 __nv_bfloat16* yo = static_cast<__nv_bfloat16*>(d.y) + (((size_t)b * d.L + t0) * d.H + h) * P + (v & ~1);
                 const float2 yl2 = make_float2(yl, yl);
@@ -768,7 +915,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                     const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
                     o[q] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
                 }
-                if (len - (c - 1) * C >= C) {             // no token of the chunk is missing
+                if (len - (cb + c - 1) * C >= C) {        // no token of the chunk is missing
 #pragma unroll
                     for (int q = 0; q < 8; ++q) *reinterpret_cast<uint32_t*>(yo + q * ystep) = o[q];
                 } else {
@@ -781,7 +928,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             const float* vec = reinterpret_cast<const float*>(sg + Lay::VEC);
             const unsigned short* sv = reinterpret_cast<const unsigned short*>(sg + Lay::V) + v;
             const unsigned short lamb = (unsigned short)(__float_as_uint(lam) >> 16);     // a power of two: exact
-            const int rows = len - c * C;                 // tokens behind them write nothing
+            const int rows = trans ? 0 : len - (cb + c) * C;      // tokens behind them write nothing
             yl = ilam * vec[3 * C + 1];
             // ---- R = V - e^Gamma rk (K S^T), 8 tokens of each half a thread
 #pragma unroll 1
@@ -789,7 +936,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 const int t0 = 32 * half + 8 * part;
                 unsigned short vt[8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) vt[q] = sv[(t0 + q) * P];
+                for (int q = 0; q < 8; ++q) vt[q] = rows > 0 ? sv[(t0 + q) * P] : 0;
                 if (t0 + 8 > rows) {
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
@@ -820,21 +967,23 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             }
             if (!ok) break;
             // ---- e^Gamma rq (Q S^T), back to its columns, while U = T R runs
-            if (!(ok = delta_wait(bar(Lay::X_Q), c, dead))) break;
-            tc_fence_after();
-            {
-                float x[16];
-                uint32_t o[16];
-                tmem_ld16(tl + Lay::XQ + 16 * part, x);
+            if constexpr (kFull) {
+                if (!(ok = delta_wait(bar(Lay::X_Q), c, dead))) break;
+                tc_fence_after();
+                {
+                    float x[16];
+                    uint32_t o[16];
+                    tmem_ld16(tl + Lay::XQ + 16 * part, x);
 #pragma unroll
-                for (int q = 0; q < 16; q += 4) {
-                    const float4 e = *reinterpret_cast<const float4*>(vec + C + 16 * part + q);
-                    const float2 a = __fmul2_rn(make_float2(e.x, e.y), make_float2(x[q], x[q + 1]));
-                    const float2 f = __fmul2_rn(make_float2(e.z, e.w), make_float2(x[q + 2], x[q + 3]));
-                    o[q] = __float_as_uint(a.x); o[q + 1] = __float_as_uint(a.y);
-                    o[q + 2] = __float_as_uint(f.x); o[q + 3] = __float_as_uint(f.y);
+                    for (int q = 0; q < 16; q += 4) {
+                        const float4 e = *reinterpret_cast<const float4*>(vec + C + 16 * part + q);
+                        const float2 a = __fmul2_rn(make_float2(e.x, e.y), make_float2(x[q], x[q + 1]));
+                        const float2 f = __fmul2_rn(make_float2(e.z, e.w), make_float2(x[q + 2], x[q + 3]));
+                        o[q] = __float_as_uint(a.x); o[q + 1] = __float_as_uint(a.y);
+                        o[q + 2] = __float_as_uint(f.x); o[q + 3] = __float_as_uint(f.y);
+                    }
+                    tmem_st16(tl + Lay::XQ + 16 * part, o);
                 }
-                tmem_st16(tl + Lay::XQ + 16 * part, o);
             }
             // ---- U: one part for Y; weighted, two parts for the state
 #pragma unroll 1
@@ -845,8 +994,11 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 float x[8];
                 tmem_ld8(tl + Lay::U + t0, x);
                 uint32_t u[4], hi[4], lo[4];
+                if constexpr (kFull) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) u[q] = pack_f16(x[2 * q], x[2 * q + 1]);
+                    for (int q = 0; q < 4; ++q) u[q] = pack_f16(x[2 * q], x[2 * q + 1]);
+                    tmem_st4(tl + Lay::UH + t0 / 2, u);
+                }
 #pragma unroll
                 for (int q = 0; q < 4; q += 2) {
                     const float4 wk = *reinterpret_cast<const float4*>(vec + 2 * C + t0 + 2 * q);
@@ -856,7 +1008,6 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 const uint32_t r = tl + Lay::UW + 32 * half + 16 * (part >> 1) + 4 * (part & 1);
                 tmem_st4(r, hi);
                 tmem_st4(r + 8, lo);
-                tmem_st4(tl + Lay::UH + t0 / 2, u);
                 tmem_st_wait();
                 arrive(Lay::U_IN0 + half);
             }
@@ -864,7 +1015,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             // ---- the state after the chunk
             const float el = vec[3 * C];
             const float2 el2 = make_float2(el, el);
-            if (!(ok = delta_wait(bar(Lay::D), c, dead))) break;
+            if (!(ok = delta_wait(bar(Lay::D), nf + c, dead))) break;
             tc_fence_after();
 #pragma unroll
             for (int n0 = 0; n0 < NQ; n0 += 16) {
@@ -875,10 +1026,12 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             }
             if (++st == ST) { st = 0; ++use; }
         }
-        if (ok) {
+        // the end state: of the segment, or, where the row ends in it, of the row
+        float* to = kFull ? (cb + max(nC, 0) == all ? d.h_out : nullptr) : trans ? nullptr : p.sloc + seg * hstep;
+        if (ok && to) {
 #pragma unroll
             for (int n = 0; n < NQ; n += 4)
-                *reinterpret_cast<float4*>(d.h_out + hoff + n) =
+                *reinterpret_cast<float4*>(to + hoff + n) =
                     make_float4(S[n / 2].x * ilam, S[n / 2].y * ilam, S[n / 2 + 1].x * ilam, S[n / 2 + 1].y * ilam);
         }
     }

@@ -97,13 +97,15 @@ def scan(lib, **over):
     a = dict(B=1, L=64, H=4, G=2, P=64, N=128, io=1, q=FAKE, ldq=256, k=FAKE + (1 << 24), ldk=256, v=FAKE + (2 << 24),
              ldv=256, dt_raw=FAKE + (3 << 24), b_raw=FAKE + (4 << 24), dt_bias=FAKE + (5 << 24),
              A_log=FAKE + (6 << 24), lengths=None, h0=None, scale=0.1, norm=1, y=FAKE + (7 << 24),
-             h_out=FAKE + (8 << 24), workspace=FAKE + (9 << 24), workspace_bytes=1 << 24, stream=None)
+             h_out=FAKE + (8 << 24), segments=0, workspace=FAKE + (9 << 24), workspace_bytes=1 << 24, stream=None)
     a.update(over)
     return lib.axon_delta_scan_fwd(*a.values())
 
 
 @pytest.mark.parametrize("over, status", [
-    (dict(B=-1), 1), (dict(L=-1), 1), (dict(H=-1), 1),
+    (dict(B=-1), 1), (dict(L=-1), 1), (dict(H=-1), 1), (dict(segments=-1), 1),
+    (dict(workspace_bytes=1000), 4), (dict(workspace=None), 1), (dict(workspace=FAKE + (9 << 24) + 8), 3),
+    (dict(workspace=FAKE + (7 << 24) + 4096), 1),
     (dict(H=5), 2), (dict(G=0), 2), (dict(P=32), 2), (dict(N=96), 2), (dict(io=2), 2), (dict(B=70000), 2),
     (dict(L=1 << 30), 2),
     (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(dt_raw=None), 1), (dict(b_raw=None), 1),
