@@ -649,30 +649,54 @@ def _token_stride(what, name, t):
     return ld
 
 
-def _used_on(stream, dev, *tensors):
-    """Tells the allocator that tensors made here are used on another stream
-    than the current one, so their memory is not handed out while it is read."""
+def _empty(stream, dev, *specs):
+    """Tensors ((shape, dtype), ...) for a call on `stream`.  Another stream
+    than the current one gets memory of its own pool (a block of the current
+    stream's might still be in use there), marked as used on the current one
+    too, where the caller reads it."""
     if stream is None:
-        return
+        return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in specs]
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(s):
+        made = [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in specs]
+    for t in made:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return made
+
+
+def _all_as(dtype, index, *tensors):
+    """Whether all tensors are of this dtype on this device, and dense."""
     for t in tensors:
-        if t is not None:
-            t.record_stream(s)
+        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            return False
+    return True
 
 
-def _delta_args(what, q, k, v, dt_raw, b_raw, params, scale):
-    H, P = v.shape[-2:]
+def _delta_args(what, q, k, v, dt_raw, b_raw, params):
+    """Sizes and pointer arguments, checked (small calls are bound by this code:
+    the common case is looked over in one go, the rest explains itself)."""
+    bias, a_log = params["dt_bias"], params["A_log"]
+    dt, i = v.dtype, v.get_device()
+    *lead, H, P = v.shape
     G, N = k.shape[-2:]
-    io = _dtype_code(v.dtype)
-    lead = tuple(v.shape[:-2])
-    dev = v.device
-    _same_device(what, dev, q=q, k=k, dt_raw=dt_raw, b_raw=b_raw, dt_bias=params["dt_bias"], A_log=params["A_log"])
-    f32 = torch.float32
-    _like(what, v.dtype, q=(q, lead + (G, N)), k=(k, lead + (G, N)), dt_raw=(dt_raw, lead + (H,)),
-          b_raw=(b_raw, lead + (H,)), dt_bias=(params["dt_bias"], (H,), f32), A_log=(params["A_log"], (H,), f32))
-    return H, P, G, N, io, (q, _token_stride(what, "q", q), k, _token_stride(what, "k", k), v,
-                            _token_stride(what, "v", v), dt_raw, b_raw, params["dt_bias"], params["A_log"]), \
-        (N ** -0.5 if scale is None else float(scale))
+    rates = (*lead, H)
+    fine = (i >= 0 and q.shape == k.shape == (*lead, G, N) and dt_raw.shape == b_raw.shape == rates and
+            bias.shape == a_log.shape == (H,) and _all_as(torch.float32, i, bias, a_log) and _all_as(dt, i, dt_raw, b_raw))
+    if fine and _all_as(dt, i, q, k, v):
+        ldq = ldk = G * N
+        ldv = H * P
+    else:
+        dev = v.device
+        _same_device(what, dev, q=q, k=k, dt_raw=dt_raw, b_raw=b_raw, dt_bias=bias, A_log=a_log)
+        f32 = torch.float32
+        _like(what, dt, q=(q, (*lead, G, N)), k=(k, (*lead, G, N)), dt_raw=(dt_raw, rates), b_raw=(b_raw, rates),
+              dt_bias=(bias, (H,), f32), A_log=(a_log, (H,), f32))
+        for t in (dt_raw, b_raw, bias, a_log):
+            if not t.is_contiguous():
+                raise ValueError(f"{what}: the rates and parameters must be contiguous")
+        ldq, ldk, ldv = (_token_stride(what, n, t) for n, t in (("q", q), ("k", k), ("v", v)))
+    return i, H, P, G, N, _dtype_code(dt), (q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, dt_raw.data_ptr(),
+                                            b_raw.data_ptr(), bias.data_ptr(), a_log.data_ptr())
 
 
 def delta_error_flag(workspace) -> int:
@@ -698,32 +722,28 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     (AXON_ERR_TIMEOUT) if a wait of the kernel gave up; ``check=False`` returns
     at once (read the flag with ``delta_error_flag(workspace)``).
     """
-    Bsz, L = v.shape[:2]
-    H, P, G, N, io, args, scale = _delta_args("delta_scan", q, k, v, dt_raw, b_raw, params, scale)
-    dev = v.device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
+    i, H, P, G, N, io, args = _delta_args("delta_scan", q, k, v, dt_raw, b_raw, params)
+    if i != torch.cuda.current_device():
+        with torch.cuda.device(i):
             return delta_scan(q, k, v, dt_raw, b_raw, params, h0, lengths=lengths, scale=scale, qk_norm=qk_norm,
                               out=out, workspace=workspace, stream=stream, segments=segments, check=check)
-    made = []
-    if out is None:
-        y = torch.empty(Bsz, L, H, P, dtype=v.dtype, device=dev)
-        h_out = torch.empty(Bsz, H, P, N, dtype=torch.float32, device=dev)
-        made += [y, h_out]
-    else:
-        y, h_out = out
-    _same_device("delta_scan", dev, h0=h0, lengths=lengths, y=y, h_out=h_out, workspace=workspace)
+    Bsz, L = v.shape[:2]
+    dev, f32 = v.device, torch.float32
+    nbytes = _lib.axon_delta_workspace_bytes(Bsz, L, H, G, P, N, io, segments)
     state = (Bsz, H, P, N)
-    _like("delta_scan", torch.float32, h0=(h0, state), h_out=(h_out, state), y=(y, v.shape, v.dtype),
-          lengths=(lengths, (Bsz,), torch.int32))
-    nbytes = axon_delta_workspace_bytes(Bsz, L, H, G, P, N, io, segments)
+    made = _empty(stream, dev, *(((v.shape, v.dtype), (state, f32)) if out is None else ()),
+                  *(((nbytes,), torch.uint8),) * (workspace is None and nbytes > 0))
+    y, h_out = out if out is not None else made[:2]
     if workspace is None and nbytes > 0:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        made.append(workspace)
+        workspace = made[-1]
+    if out is not None or h0 is not None or lengths is not None:
+        _same_device("delta_scan", dev, h0=h0, lengths=lengths, y=y, h_out=h_out, workspace=workspace)
+        _like("delta_scan", f32, h0=(h0, state), h_out=(h_out, state), y=(y, v.shape, v.dtype),
+              lengths=(lengths, (Bsz,), torch.int32))
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    axon_delta_scan_fwd(Bsz, L, H, G, P, N, io, *args, lengths, h0, scale, int(qk_norm), y, h_out, segments, workspace,
-                        wsz, stream=stream)
-    _used_on(stream, dev, *made)
+    _check(_lib.axon_delta_scan_fwd(Bsz, L, H, G, P, N, io, *args, _p(lengths), _p(h0),
+                                    N ** -0.5 if scale is None else scale, qk_norm, _p(y), _p(h_out), segments,
+                                    _p(workspace), wsz, _stream(stream)), "axon_delta_scan_fwd")
     if check and nbytes > 0 and delta_error_flag(workspace) != 0:
         raise AxonError(6, "axon_delta_scan_fwd (a wait for a copy or a tensor-core product gave up)")
     return y, h_out
@@ -733,20 +753,21 @@ def delta_step(q, k, v, dt_raw, b_raw, params: dict, state, *, scale=None, qk_no
     """One cached step of the gated delta rule: q, k (B,G,N), v (B,H,P),
     dt_raw, b_raw (B,H); ``state`` (B,H,P,N) float32 is updated in place.
     Returns y (B,H,P)."""
-    Bsz = v.shape[0]
-    H, P, G, N, io, args, scale = _delta_args("delta_step", q, k, v, dt_raw, b_raw, params, scale)
-    dev = v.device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
+    i, H, P, G, N, io, args = _delta_args("delta_step", q, k, v, dt_raw, b_raw, params)
+    if i != torch.cuda.current_device():
+        with torch.cuda.device(i):
             return delta_step(q, k, v, dt_raw, b_raw, params, state, scale=scale, qk_norm=qk_norm, y=y, stream=stream)
-    made = y is None
-    if made:
-        y = torch.empty(Bsz, H, P, dtype=v.dtype, device=dev)
-    _same_device("delta_step", dev, state=state, y=y)
-    _like("delta_step", torch.float32, state=(state, (Bsz, H, P, N)), y=(y, (Bsz, H, P), v.dtype))
-    axon_delta_step(Bsz, H, G, P, N, io, *args, scale, int(qk_norm), state, y, stream=stream)
-    if made:
-        _used_on(stream, dev, y)
+    Bsz = v.shape[0]
+    if y is None:
+        y = _empty(stream, v.device, (v.shape, v.dtype))[0]
+    elif y.shape != v.shape or y.dtype is not v.dtype or y.get_device() != i:
+        _same_device("delta_step", v.device, y=y)
+        _like("delta_step", v.dtype, y=(y, v.shape))
+    if state.shape != (Bsz, H, P, N) or state.dtype is not torch.float32 or state.get_device() != i:
+        _same_device("delta_step", v.device, state=state)
+        _like("delta_step", torch.float32, state=(state, (Bsz, H, P, N)))
+    _check(_lib.axon_delta_step(Bsz, H, G, P, N, io, *args, N ** -0.5 if scale is None else scale, qk_norm, _p(state),
+                                _p(y), _stream(stream)), "axon_delta_step")
     return y
 
 
@@ -785,27 +806,34 @@ def gated_norm(x, weight=None, z=None, *, bias=None, group=None, kind="rms", gat
     form.  x, z and out may be slices with a row stride; out may be x or z.
     """
     C = x.shape[-1]
-    D = C if group is None else int(group)
-    dev = x.device
-    _same_device("gated_norm", dev)
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
+    D = C if group is None else group
+    i = x.get_device()
+    if i < 0:
+        _same_device("gated_norm", x.device)
+    if i != torch.cuda.current_device():
+        with torch.cuda.device(i):
             return gated_norm(x, weight, z, bias=bias, group=group, kind=kind, gate=gate, act=act, eps=eps, out=out,
                               stream=stream)
-    made = out is None
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if made else out
-    _same_device("gated_norm", dev, weight=weight, bias=bias, z=z, out=y)
-    forms = {t.numel() for t in (weight, bias) if t is not None}
-    if len(forms) > 1 or not forms <= {D, C}:
-        raise ValueError(f"gated_norm: weight and bias need {D} or {C} values, both the same")
-    n = forms.pop() if forms else D
-    _like("gated_norm", torch.float32, weight=(weight, (n,)), bias=(bias, (n,)), z=(z, x.shape, x.dtype),
-          out=(y, x.shape, x.dtype))
+    y = _empty(stream, x.device, (x.shape, x.dtype))[0] if out is None else out
+    n = D if weight is None and bias is None else (bias if weight is None else weight).shape[0]
+    if n != D and n != C:
+        raise ValueError(f"gated_norm: weight and bias need {D} or {C} values, not {n}")
     rows = x.numel() // C if C else 0
-    axon_gated_norm_fwd(rows, C, D, _dtype_code(x.dtype), NORM_KINDS[kind], NORM_GATES[gate] if z is not None else 0,
-                        int(act), x, _row_stride("gated_norm", "x", x, rows, C), z,
-                        0 if z is None else _row_stride("gated_norm", "z", z, rows, C), weight, bias,
-                        int(n == C and n != D), eps, y, _row_stride("gated_norm", "out", y, rows, C), stream=stream)
-    if made:
-        _used_on(stream, dev, y)
+    params = [t for t in (weight, bias) if t is not None]
+    data = [x, y] if z is None else [x, y, z]
+    if (_all_as(torch.float32, i, *params) and all(t.shape == (n,) for t in params) and _all_as(x.dtype, i, *data) and
+            all(t.shape == x.shape for t in data)):
+        ldx = ldy = ldz = C
+    else:
+        _same_device("gated_norm", x.device, weight=weight, bias=bias, z=z, out=y)
+        _like("gated_norm", torch.float32, weight=(weight, (n,)), bias=(bias, (n,)), z=(z, x.shape, x.dtype),
+              out=(y, x.shape, x.dtype))
+        for t in params:
+            if not t.is_contiguous():
+                raise ValueError("gated_norm: weight and bias must be contiguous")
+        ldx, ldy, ldz = (0 if t is None else _row_stride("gated_norm", name, t, rows, C)
+                         for name, t in (("x", x), ("out", y), ("z", z)))
+    _check(_lib.axon_gated_norm_fwd(rows, C, D, _dtype_code(x.dtype), NORM_KINDS[kind], 0 if z is None else NORM_GATES[gate],
+                                    act, x.data_ptr(), ldx, _v(z), ldz, _v(weight), _v(bias), n == C and n != D, eps,
+                                    y.data_ptr(), ldy, _stream(stream)), "axon_gated_norm_fwd")
     return y

@@ -100,8 +100,10 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // Segments of whole chunks.  One walk runs on an SM at a time, so a pass takes
 // ceil(walks / SMs) rounds of one segment's chunks; a chunk of the pass
-// without outputs costs about 2/3 of one with them, a fold about half a chunk,
-// and the second launch about two.  `requested` > 0 asks for that many.
+// without outputs takes as long as one with them (2.9 us: the same chain of
+// products and conversions), a round's start about 2.5 chunks, a fold half of
+// one, and the second launch about two.  B1 L4096 H32 measured 247, 236, 186, 205, 230 us at 1 to 5
+// segments.  `requested` > 0 asks for that many.
 struct DeltaPlan {
     int segs, cps;
 };
@@ -120,7 +122,7 @@ DeltaPlan delta_plan(int B, int L, int H, int requested) {
     for (int want = 1; want <= most; ++want) {
         const DeltaPlan p = cut(want);
         const long long full = (p.segs * walks + sms - 1) / sms, state = ((2 * p.segs - 3) * walks + sms - 1) / sms;
-        const double t = full * p.cps + (p.segs > 1 ? 0.67 * state * p.cps + 0.5 * (p.segs - 2) + 2.0 : 0.0);
+        const double t = full * (p.cps + 2.5) + (p.segs > 1 ? state * (p.cps + 2.5) + 0.5 * (p.segs - 2) + 2.0 : 0.0);
         if (t < least) {
             least = t;
             best = p;
@@ -208,8 +210,8 @@ template <class Io>
 void launch_norm(const NormParams& p, cudaStream_t st) {
     const int pieces = p.D / NormVec<Io>::VE;
     auto warps = [&](auto kernel, int LG, int U) {
-        const int per_block = 8 * (32 / LG) * U;
-        kernel<<<(unsigned)((p.groups + per_block - 1) / per_block), 256, 0, st>>>(p);
+        const int per_block = 2 * (32 / LG) * U;
+        kernel<<<(unsigned)((p.groups + per_block - 1) / per_block), 64, 0, st>>>(p);
     };
     if (pieces <= 4) warps(gated_norm_kernel<Io, 4, 1, 4, 1>, 4, 4);
     else if (pieces <= 8) warps(gated_norm_kernel<Io, 8, 1, 4, 1>, 8, 4);

@@ -163,7 +163,13 @@ __device__ __forceinline__ void delta_invert(float* A, float* W, int tid) {
             const float* row = A + (o + i) * LDA + o;
             float acc = i == j ? 1.f : 0.f;
 #pragma unroll
-            for (int k = 0; k < i; ++k) acc = fmaf(-row[k], t[k], acc);
+            for (int k = 0; k < i; k += 4) {             // what the row holds from its diagonal on is 0
+                const float4 x4 = *reinterpret_cast<const float4*>(row + k);
+                acc = fmaf(-x4.x, t[k], acc);
+                if (k + 1 < i) acc = fmaf(-x4.y, t[k + 1], acc);
+                if (k + 2 < i) acc = fmaf(-x4.z, t[k + 2], acc);
+                if (k + 3 < i) acc = fmaf(-x4.w, t[k + 3], acc);
+            }
             t[i] = acc;
         }
         __syncwarp();
@@ -176,20 +182,28 @@ __device__ __forceinline__ void delta_invert(float* A, float* W, int tid) {
         float* w = W + (tid >> 6) * 16 * LDW;
         float* row = A + (o + 16 + r) * LDA + o;         // of A21, then of T22 16 columns on
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
-            const float x = row[k];
-            const float4 y = *reinterpret_cast<const float4*>(A + (o + k) * LDA + o + c);
-            s.x = fmaf(x, y.x, s.x); s.y = fmaf(x, y.y, s.y); s.z = fmaf(x, y.z, s.z); s.w = fmaf(x, y.w, s.w);
+#pragma unroll 1
+        for (int k = 0; k < 16; k += 4) {
+            const float4 x4 = *reinterpret_cast<const float4*>(row + k);
+            const float xk[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 y = *reinterpret_cast<const float4*>(A + (o + k + q) * LDA + o + c);
+                s.x = fmaf(xk[q], y.x, s.x); s.y = fmaf(xk[q], y.y, s.y); s.z = fmaf(xk[q], y.z, s.z); s.w = fmaf(xk[q], y.w, s.w);
+            }
         }
         *reinterpret_cast<float4*>(w + r * LDW + c) = s;
         __syncthreads();
         s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
-            const float x = -row[16 + k];
-            const float4 y = *reinterpret_cast<const float4*>(w + k * LDW + c);
-            s.x = fmaf(x, y.x, s.x); s.y = fmaf(x, y.y, s.y); s.z = fmaf(x, y.z, s.z); s.w = fmaf(x, y.w, s.w);
+#pragma unroll 1
+        for (int k = 0; k < 16; k += 4) {
+            const float4 x4 = *reinterpret_cast<const float4*>(row + 16 + k);
+            const float xk[4] = {-x4.x, -x4.y, -x4.z, -x4.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 y = *reinterpret_cast<const float4*>(w + (k + q) * LDW + c);
+                s.x = fmaf(xk[q], y.x, s.x); s.y = fmaf(xk[q], y.y, s.y); s.z = fmaf(xk[q], y.z, s.z); s.w = fmaf(xk[q], y.w, s.w);
+            }
         }
         *reinterpret_cast<float4*>(row + c) = s;
     }
@@ -200,21 +214,29 @@ __device__ __forceinline__ void delta_invert(float* A, float* W, int tid) {
         float* row = A + (32 + r) * LDA;
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {           // W = A21 T11, then T21 = -T22 W
-            float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            float2 s[4] = {};
             const float* x = row + 32 * pass;
             const float* y = pass ? W + c : A + c;
             const int ldy = pass ? LDW : LDA;
-#pragma unroll 4
-            for (int k = 0; k < (pass ? kend : 32); ++k) {
-                const float xv = x[k];
-                const float4 y0 = *reinterpret_cast<const float4*>(y + k * ldy), y1 = *reinterpret_cast<const float4*>(y + k * ldy + 4);
-                s[0] = fmaf(xv, y0.x, s[0]); s[1] = fmaf(xv, y0.y, s[1]); s[2] = fmaf(xv, y0.z, s[2]); s[3] = fmaf(xv, y0.w, s[3]);
-                s[4] = fmaf(xv, y1.x, s[4]); s[5] = fmaf(xv, y1.y, s[5]); s[6] = fmaf(xv, y1.z, s[6]); s[7] = fmaf(xv, y1.w, s[7]);
+#pragma unroll 2
+            for (int k = 0; k < (pass ? kend : 32); k += 4) {
+                const float4 x4 = *reinterpret_cast<const float4*>(x + k);
+                const float xk[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 y0 = *reinterpret_cast<const float4*>(y + (k + q) * ldy);
+                    const float4 y1 = *reinterpret_cast<const float4*>(y + (k + q) * ldy + 4);
+                    const float2 xx = make_float2(xk[q], xk[q]);
+                    s[0] = __ffma2_rn(xx, make_float2(y0.x, y0.y), s[0]);
+                    s[1] = __ffma2_rn(xx, make_float2(y0.z, y0.w), s[1]);
+                    s[2] = __ffma2_rn(xx, make_float2(y1.x, y1.y), s[2]);
+                    s[3] = __ffma2_rn(xx, make_float2(y1.z, y1.w), s[3]);
+                }
             }
             const float f = pass ? -1.f : 1.f;
             float* out = pass ? row + c : W + r * LDW + c;
-            *reinterpret_cast<float4*>(out) = make_float4(f * s[0], f * s[1], f * s[2], f * s[3]);
-            *reinterpret_cast<float4*>(out + 4) = make_float4(f * s[4], f * s[5], f * s[6], f * s[7]);
+            *reinterpret_cast<float4*>(out) = make_float4(f * s[0].x, f * s[0].y, f * s[1].x, f * s[1].y);
+            *reinterpret_cast<float4*>(out + 4) = make_float4(f * s[2].x, f * s[2].y, f * s[3].x, f * s[3].y);
             __syncthreads();
         }
     }
