@@ -519,7 +519,7 @@ struct DeltaWalkSmem {
     static constexpr int VM = kDlStages * STAGE;          // largest |v| of the columns, per stage
     static constexpr int SMAX = VM + kDlStages * P * 4;   // largest |S| of the quarters of a lane's state row
     static constexpr int MB = SMAX + 4 * 128 * 4;
-    enum { FULL, VMAX = FULL + kDlStages, X_K0 = VMAX + kDlStages, X_K1, X_Q, U_0, U_1, Y_M, D, S_IN, R_IN0, R_IN1, U_IN0,
+    enum { FULL, VMAX = FULL + kDlStages, X_K0 = VMAX + kDlStages, X_K1, X_Q, U_0, U_1, Y_M, D, D_HI, S_IN, R_IN0, R_IN1, U_IN0,
            U_IN1, Y_OUT, QUAD, DRAIN = QUAD + 4, TR_FULL, BARS = TR_FULL + 2 };
     static constexpr int DEAD = MB + 8 * BARS;            // a wait gave up
     static constexpr int SLOT = DEAD + 4;
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             load_chunk(loaded++, 0);                      // the other stages hold the transitions first
         constexpr uint32_t kId64 = umma_idesc_f16(128, 64, 0, 0);    // B K-major: K', Q', T, M rows
         constexpr uint32_t kId32 = umma_idesc_f16(128, 32, 0, 0);
-        constexpr uint32_t kIdS = umma_idesc_f16(128, N, 0, 1);      // B: K' rows as the K dimension (MN-major)
+        constexpr uint32_t kIdS = umma_idesc_f16(128, 64, 0, 1);      // B: K' rows as the K dimension (MN-major)
         // matrix descriptors of the first stage; an offset within shared memory
         // adds to their address field, so a step costs one addition
         const uint64_t d_k = umma_desc(sb + Lay::K, 16, 1024), d_ks = umma_desc(sb + Lay::K, 8192, 1024);
@@ -725,17 +725,24 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             // the increment goes where S is: Q S^T has to be done with it
             if (!(ok = (!kFull || delta_wait(bar(Lay::X_Q), c, dead)) && delta_wait(bar(Lay::U_IN0), c, dead))) break;
             tc_fence_after();
-            auto increment = [&](int half) {              // U_w^T K, 16 tokens a step, hi and lo
+            auto increment = [&](int half, int n) {       // U_w^T K, n .. n + 63, 16 tokens a step, hi and lo
 #pragma unroll
                 for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                    umma_ts(tb + Lay::DD, tb + Lay::UW + 8 * ks, at(ks_d, (ks >> 1) * 2048), kIdS, ks > 0);
+                    umma_ts(tb + Lay::DD + n, tb + Lay::UW + 8 * ks, at(ks_d, n * 128 + (ks >> 1) * 2048), kIdS, ks > 0);
             };
-            if (elect_one()) increment(0);
+            if (elect_one()) {
+                increment(0, 0);
+                if (N == 128) increment(0, 64);
+            }
             if (!(ok = delta_wait(bar(Lay::U_IN1), c, dead))) break;
             tc_fence_after();
             if (elect_one()) {
-                increment(1);
-                umma_commit(bar(Lay::D));
+                increment(1, 0);
+                umma_commit(bar(Lay::D));                 // the first half of the state's threads can go on
+                if (N == 128) {
+                    increment(1, 64);
+                    umma_commit(bar(Lay::D_HI));
+                }
                 if constexpr (kFull) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)        // Y += M U
@@ -988,11 +995,11 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 arrive(Lay::R_IN0 + half);
             }
             if (!ok) break;
-            // ---- e^Gamma rq (Q S^T), back to its columns, while U = T R runs
-            if constexpr (kFull) {
-                if (!(ok = delta_wait(bar(Lay::X_Q), c, dead))) break;
-                tc_fence_after();
-                {
+            // ---- U: one part for Y; weighted, two parts for the state
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (kFull && half == 1) {
+                    // e^Gamma rq (Q S^T), which was done before U, back to its columns while U's second half runs
                     float x[16];
                     uint32_t o[16];
                     tmem_ld16(tl + Lay::XQ + 16 * part, x);
@@ -1006,10 +1013,6 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                     }
                     tmem_st16(tl + Lay::XQ + 16 * part, o);
                 }
-            }
-            // ---- U: one part for Y; weighted, two parts for the state
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
                 if (!(ok = delta_wait(bar(Lay::U_0 + half), c, dead))) break;
                 tc_fence_after();
                 const int t0 = 32 * half + 8 * part;
@@ -1037,14 +1040,20 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             // ---- the state after the chunk
             const float el = vec[3 * C];
             const float2 el2 = make_float2(el, el);
-            if (!(ok = delta_wait(bar(Lay::D), nf + c, dead))) break;
+            if (!(ok = N == 128 && part >= 2 ? delta_wait(bar(Lay::D_HI), c, dead) : delta_wait(bar(Lay::D), nf + c, dead))) break;
             tc_fence_after();
+            if constexpr (NQ == 32) {
+                uint32_t x[32];
+                tmem_ld32_async(tl + Lay::DD + NQ * part, x);
+                tmem_wait_ld();
 #pragma unroll
-            for (int n0 = 0; n0 < NQ; n0 += 16) {
+                for (int q = 0; q < 16; ++q)
+                    S[q] = __ffma2_rn(el2, S[q], make_float2(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1])));
+            } else {
                 float x[16];
-                tmem_ld16(tl + Lay::DD + NQ * part + n0, x);
+                tmem_ld16(tl + Lay::DD + NQ * part, x);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) S[n0 / 2 + q] = __ffma2_rn(el2, S[n0 / 2 + q], make_float2(x[2 * q], x[2 * q + 1]));
+                for (int q = 0; q < 8; ++q) S[q] = __ffma2_rn(el2, S[q], make_float2(x[2 * q], x[2 * q + 1]));
             }
             if (++st == ST) { st = 0; ++use; }
         }
