@@ -81,6 +81,7 @@ def ref(inp, h0=True, lengths=None, qk_norm=True, scale=None):
 def check(inp, what, state_tol=1e-5, **kw):
     y, h = run(inp, **kw)
     kw.pop("in_place", None)
+    kw.pop("segments", None)
     y_ref, h_ref = ref(inp, **kw)
     io = "f32" if inp["v"].dtype == torch.float32 else "bf16"
     ln = kw.get("lengths")
@@ -251,6 +252,95 @@ def test_two_calls_and_streams_agree(cuda_lib, io):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, out[0]) and torch.equal(h, out[1])
+
+
+# ------------------------------------------------------------ chunks and segments
+@pytest.mark.parametrize("segments", [1, 2, 3, 4, 7, 64])
+@pytest.mark.parametrize("N, P", [(64, 64), (64, 128), (128, 64), (128, 128)])
+def test_segments(cuda_lib, segments, N, P):
+    """Any cut of the sequence (7 chunks, the last ragged) gives the same answer."""
+    check(make(N, P, 2, 4, L=430, B=1), f"{segments} segments, N{N} P{P}", segments=segments)
+
+
+@pytest.mark.parametrize("segments", [2, 3, 7])
+def test_segments_of_ragged_rows(cuda_lib, segments):
+    """Rows that end in every segment, before a segment's first token and at its
+    last, and a row of no tokens; the state in place."""
+    lengths = [0, 1, 64, 65, 128, 190, 192, 193, 320, 430]
+    inp = make(G=1, H=2, B=len(lengths), L=430)
+    check(inp, f"{segments} segments", segments=segments, lengths=lengths)
+    check(inp, f"{segments} segments in place", segments=segments, lengths=lengths, in_place=True)
+
+
+def test_error_flag_stays_clear(cuda_lib):
+    from selective_state_space_52_b200 import axon_ssm
+    d, params = dev(make(L=300, B=1))
+    for segments in (1, 3):
+        n = axon_ssm.axon_delta_workspace_bytes(1, 300, 4, 2, 128, 128, axon_ssm.AXON_BF16, segments)
+        ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")        # a nonzero flag beforehand, garbage in the rest
+        y, h = axon_ssm.delta_scan(*(d[k] for k in SEQ), params, d["h0"], workspace=ws, segments=segments)
+        assert axon_ssm.delta_error_flag(ws) == 0
+        assert torch.isfinite(y).all() and torch.isfinite(h).all()
+
+
+@pytest.mark.parametrize("segments", [1, 3])
+@pytest.mark.parametrize("power", [-60, -20, 20, 60])
+def test_scaled_values(cuda_lib, power, segments):
+    """Everything is linear in v and h0: values of any size, through the lanes' scales."""
+    inp = make(L=300, B=1)
+    inp["v"] = (inp["v"].float() * 2.0 ** power).bfloat16()
+    inp["h0"] = inp["h0"] * 2.0 ** power
+    check(inp, f"values times 2^{power}", segments=segments)
+
+
+@pytest.mark.parametrize("segments", [1, 3])
+def test_outliers_in_v(cuda_lib, segments):
+    """Columns of very different size, and single values far above the rest of
+    their column, so that lanes rescale on the way; each size is checked by itself."""
+    inp = make(L=400, B=1, H=2, G=1)
+    size = torch.logspace(-6, 6, 128)
+    inp["v"] = (inp["v"].float() * size).bfloat16()
+    inp["v"][0, 100, :, ::7] = (1e5 * size[::7]).bfloat16()
+    inp["v"][0, 101, :, 3::11] = 0
+    inp["h0"] = inp["h0"] * size[:, None]
+    y, h = run(inp, segments=segments)
+    y_ref, h_ref = ref(inp)
+    for v in range(0, 128, 5):
+        close(y[..., v], y_ref[..., v], 2.6e-3, f"y of column {v}", 2e-2)
+        close(h[:, :, v], h_ref[:, :, v], 1e-5, f"state of column {v}")
+
+
+def test_silent_stretch(cuda_lib):
+    """No values for 200 tokens: the state only decays and forgets what the keys
+    touch.  A lane's numbers are kept to 2^-21 of its largest at the start of a
+    chunk, and 21 chunks' worth of such errors stay below 1e-5 of the state
+    before the stretch (nothing brings them up: the map never lengthens a row)."""
+    inp = make(L=200, B=1)
+    inp["v"][:] = 0
+    y, h = run(inp)
+    y_ref, h_ref = ref(inp)
+    assert np.abs(h - h_ref).max() <= 1e-5 * np.abs(inp["h0"].numpy()).max()
+    close(y, y_ref, 2.6e-3, "y", 1.3e-2)
+
+
+def test_long_offsets(cuda_lib):
+    """2^31 values of v and of y: the last head of the wide call, bit for bit what
+    a call on that head alone gives (it reads the same tensors at their strides)."""
+    from selective_state_space_52_b200 import axon_ssm
+    L, H, P, N = 131072, 128, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(9)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16)
+
+    q, k, v = normal(1, L, 1, N), normal(1, L, 1, N), normal(1, L, H, P)
+    dt_raw, b_raw = normal(1, L, H), normal(1, L, H)
+    params = {"dt_bias": torch.full((H,), -4.0, device="cuda"), "A_log": torch.linspace(0, 2, H, device="cuda")}
+    y, h = axon_ssm.delta_scan(q, k, v, dt_raw, b_raw, params, segments=1)
+    one = {n: t[-1:].clone() for n, t in params.items()}
+    y1, h1 = axon_ssm.delta_scan(q, k, v[:, :, -1:], dt_raw[..., -1:].contiguous(), b_raw[..., -1:].contiguous(), one, segments=1)
+    assert torch.equal(y[:, :, -1:], y1) and torch.equal(h[:, -1:], h1)
+    assert torch.isfinite(y1).all() and float(y1[:, -1].float().abs().max()) > 0
 
 
 # ------------------------------------------------------------ the cached step

@@ -127,6 +127,22 @@ def test_delta_scan_rejects_strided_overlap(lib):
     assert scan(lib, ldv=4096, y=FAKE + (2 << 24) + 4096 * 2 * 62 + 1024) == 1
 
 
+def test_delta_workspace_query(lib):
+    q = lib.axon_delta_workspace_bytes
+    chunk = lambda G, H, N: G * 128 * N * 2 + H * 25600             # noqa: E731
+    # whole sequences: the flag's 256 bytes and every chunk's tiles
+    assert q(1, 640, 4, 2, 128, 128, 1, 1) == 256 + 10 * chunk(2, 4, 128)
+    assert q(3, 65, 5, 5, 64, 64, 1, 1) == 256 + 6 * chunk(5, 5, 64)
+    # three segments: two end states, one transition with its row scales, h0 again
+    state = 4 * 64 * 128 * 4
+    assert q(1, 640, 4, 2, 64, 128, 1, 3) == 256 + 10 * chunk(2, 4, 128) + 2 * state + 4 * 4 * 128 * 128 + 4 * 128 * 4 + state
+    assert q(1, 640, 4, 2, 128, 128, 0, 0) == 0                     # float32: token by token
+    assert q(1, 8, 4, 2, 128, 128, 1, 0) == 0                       # so are a few tokens
+    for bad in ((-1, 64, 4, 2, 128, 128, 1, 0), (1, 64, 5, 2, 128, 128, 1, 0), (1, 64, 4, 2, 96, 128, 1, 0),
+                (1, 64, 4, 2, 128, 128, 1, -1)):
+        assert q(*bad) == 0
+
+
 def test_delta_noop_sizes(lib):
     assert scan(lib, B=0) == 0
     assert scan(lib, H=0) == 0
