@@ -450,7 +450,8 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * `segments` runs of whole chunks (0: chosen for the current device; at most
  * 64 and one per chunk): a first launch walks all but the last for their end
  * states and transitions, and the walk of each segment enters with the fold of
- * those before it.  float32 and very short sequences go token by token.
+ * those before it.  float32 sequences, and short ones unless `segments` > 0,
+ * go token by token.
  *
  * `workspace` (16-byte aligned; may be NULL when the size is 0) holds
  * axon_delta_workspace_bytes(B, L, H, G, P, N, io, segments) bytes for the

@@ -664,6 +664,14 @@ def _empty(stream, dev, *specs):
     return made
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _stream_on(stream, index):
+    """The raw stream handle; the current one of the (current) device `index` by default."""
+    return _raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream)
+
+
 def _all_as(dtype, index, *tensors):
     """Whether all tensors are of this dtype on this device, and dense."""
     for t in tensors:
@@ -723,7 +731,7 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     at once (read the flag with ``delta_error_flag(workspace)``).
     """
     i, H, P, G, N, io, args = _delta_args("delta_scan", q, k, v, dt_raw, b_raw, params)
-    if i != torch.cuda.current_device():
+    if i != _current_device():
         with torch.cuda.device(i):
             return delta_scan(q, k, v, dt_raw, b_raw, params, h0, lengths=lengths, scale=scale, qk_norm=qk_norm,
                               out=out, workspace=workspace, stream=stream, segments=segments, check=check)
@@ -743,7 +751,7 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.axon_delta_scan_fwd(Bsz, L, H, G, P, N, io, *args, _p(lengths), _p(h0),
                                     N ** -0.5 if scale is None else scale, qk_norm, _p(y), _p(h_out), segments,
-                                    _p(workspace), wsz, _stream(stream)), "axon_delta_scan_fwd")
+                                    _p(workspace), wsz, _stream_on(stream, i)), "axon_delta_scan_fwd")
     if check and nbytes > 0 and delta_error_flag(workspace) != 0:
         raise AxonError(6, "axon_delta_scan_fwd (a wait for a copy or a tensor-core product gave up)")
     return y, h_out
@@ -754,7 +762,7 @@ def delta_step(q, k, v, dt_raw, b_raw, params: dict, state, *, scale=None, qk_no
     dt_raw, b_raw (B,H); ``state`` (B,H,P,N) float32 is updated in place.
     Returns y (B,H,P)."""
     i, H, P, G, N, io, args = _delta_args("delta_step", q, k, v, dt_raw, b_raw, params)
-    if i != torch.cuda.current_device():
+    if i != _current_device():
         with torch.cuda.device(i):
             return delta_step(q, k, v, dt_raw, b_raw, params, state, scale=scale, qk_norm=qk_norm, y=y, stream=stream)
     Bsz = v.shape[0]
@@ -767,7 +775,7 @@ def delta_step(q, k, v, dt_raw, b_raw, params: dict, state, *, scale=None, qk_no
         _same_device("delta_step", v.device, state=state)
         _like("delta_step", torch.float32, state=(state, (Bsz, H, P, N)))
     _check(_lib.axon_delta_step(Bsz, H, G, P, N, io, *args, N ** -0.5 if scale is None else scale, qk_norm, _p(state),
-                                _p(y), _stream(stream)), "axon_delta_step")
+                                _p(y), _stream_on(stream, i)), "axon_delta_step")
     return y
 
 
@@ -810,7 +818,7 @@ def gated_norm(x, weight=None, z=None, *, bias=None, group=None, kind="rms", gat
     i = x.get_device()
     if i < 0:
         _same_device("gated_norm", x.device)
-    if i != torch.cuda.current_device():
+    if i != _current_device():
         with torch.cuda.device(i):
             return gated_norm(x, weight, z, bias=bias, group=group, kind=kind, gate=gate, act=act, eps=eps, out=out,
                               stream=stream)
@@ -835,5 +843,5 @@ def gated_norm(x, weight=None, z=None, *, bias=None, group=None, kind="rms", gat
                          for name, t in (("x", x), ("out", y), ("z", z)))
     _check(_lib.axon_gated_norm_fwd(rows, C, D, _dtype_code(x.dtype), NORM_KINDS[kind], 0 if z is None else NORM_GATES[gate],
                                     act, x.data_ptr(), ldx, _v(z), ldz, _v(weight), _v(bias), n == C and n != D, eps,
-                                    y.data_ptr(), ldy, _stream(stream)), "axon_gated_norm_fwd")
+                                    y.data_ptr(), ldy, _stream_on(stream, i)), "axon_gated_norm_fwd")
     return y

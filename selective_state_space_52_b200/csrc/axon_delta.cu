@@ -91,10 +91,21 @@ void launch_recur(const DeltaParams& p, cudaStream_t st) {
         delta_recur_kernel<Io, N, 1><<<dim3((unsigned)(p.P / ROWS1), (unsigned)p.H, (unsigned)p.B), 128, 0, st>>>(p);
 }
 
-// bf16 sequences of at least this many tokens go in chunks.
-constexpr int kChunkedFrom = 32;
 constexpr int kDlMaxSegs = 64;
-bool chunked(int L, axon_dtype io) { return io == AXON_BF16 && L >= kChunkedFrom; }
+// Whether bf16 sequences go in chunks: on request (segments > 0), or when that
+// is faster.  Measured, in us, with x = B H P N / 128^2: a token of the
+// token-by-token kernel takes 0.15 + 0.0035 x; one chunk costs 23 (N = 128) or
+// 14 (N = 64), most of it the start of two launches, or a SM's share of that
+// with many heads, and each further one 3.  (B1 H8: 64 tokens 15 against 24,
+// 128 tokens 27 against 26; B8 H16: 32 tokens 22 against 24, 48 tokens 31
+// against 24; B32 H32: 24 tokens 100 against 115, 32 tokens 127 against 116.)
+bool chunked(int B, int L, int H, int P, int N, axon_dtype io, int segments) {
+    if (io != AXON_BF16 || L <= 0) return false;
+    if (segments > 0) return true;
+    const double bh = (double)B * H, x = bh * P * N / 16384.0;
+    const double chunks = (N == 128 ? 23.0 : 14.0) * std::max(1.0, bh / 205.0) + 3.0 * ((L - 1) / kDlC);
+    return chunks < L * (0.15 + 0.0035 * x);
+}
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -232,7 +243,7 @@ using namespace axon;
 extern "C" {
 
 size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io, int segments) {
-    if (B <= 0 || L < 0 || H <= 0 || segments < 0 || !shape_ok(H, G, P, N) || !chunked(L, io)) return 0;
+    if (B <= 0 || L < 0 || H <= 0 || segments < 0 || !shape_ok(H, G, P, N) || !chunked(B, L, H, P, N, io, segments)) return 0;
     return delta_ws(B, L, H, G, P, N, delta_plan(B, L, H, segments)).total;
 }
 
@@ -253,7 +264,8 @@ axon_status axon_delta_scan_fwd(int B, int L, int H, int G, int P, int N, axon_d
         return AXON_ERR_ALIGNMENT;
     const DeltaPlan plan = delta_plan(B, L, H, segments);
     const DeltaWs w = delta_ws(B, L, H, G, P, N, plan);
-    const size_t n_ws = chunked(L, io) ? w.total : 0;
+    const bool by_chunks = chunked(B, L, H, P, N, io, segments);
+    const size_t n_ws = by_chunks ? w.total : 0;
     if (workspace_bytes < n_ws) return AXON_ERR_WORKSPACE;
     if (n_ws > 0 && !workspace) return AXON_ERR_INVALID_ARG;
     const size_t es = io == AXON_BF16 ? 2 : 4;
@@ -271,7 +283,7 @@ axon_status axon_delta_scan_fwd(int B, int L, int H, int G, int P, int N, axon_d
 
     DeltaParams p{B, L, H, G, P, ldq, ldk, ldv, q, k, v, dt_raw, b_raw, dt_bias, A_log, lengths, h0, y, h_out, scale, qk_norm != 0};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (chunked(L, io)) {
+    if (by_chunks) {
         unsigned char* ws = static_cast<unsigned char*>(workspace);
         const bool split = plan.segs > 1;
         const DeltaChunkParams c{p, (L + kDlC - 1) / kDlC, ws + w.kq, ws + w.blob, reinterpret_cast<int*>(ws + w.err),

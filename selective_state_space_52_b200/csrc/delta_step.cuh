@@ -192,14 +192,15 @@ __global__ void __launch_bounds__(128) delta_recur_kernel(DeltaParams p) {
     if (p.lengths) len = min(max(__ldg(p.lengths + b), 0), p.L);
 
     const size_t hoff = (((size_t)b * p.H + h) * p.P + blk0 + loc0) * N + 4 * qd;
-    float S[RT][16];
+    float2 S[RT][8];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float4 v = p.h0 ? *reinterpret_cast<const float4*>(p.h0 + hoff + (size_t)r * RW * N + 4 * LPR * i)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[r][4 * i] = v.x; S[r][4 * i + 1] = v.y; S[r][4 * i + 2] = v.z; S[r][4 * i + 3] = v.w;
+            S[r][2 * i] = make_float2(v.x, v.y);
+            S[r][2 * i + 1] = make_float2(v.z, v.w);
         }
 
     const T* qg = static_cast<const T*>(p.q) + (size_t)b * p.L * p.ldq + (size_t)g * N;
@@ -264,34 +265,53 @@ __global__ void __launch_bounds__(128) delta_recur_kernel(DeltaParams p) {
             }
         }
         __syncthreads();
+        float2 k[8], q[8];
+        auto token = [&](int t) {
+            float r[16];
+            delta_load16<Io, LPR>(sk + t * N, qd, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[i] = make_float2(r[2 * i], r[2 * i + 1]);
+            delta_load16<Io, LPR>(sq + t * N, qd, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = make_float2(r[2 * i], r[2 * i + 1]);
+        };
         for (int t = 0; t < nt; ++t) {
-            float k[16], q[16];
-            delta_load16<Io, LPR>(sk + t * N, qd, k);
-            delta_load16<Io, LPR>(sq + t * N, qd, q);
+            token(t);
             const float4 c = sc[t];
             const float kq = skq[t];
             float dk[RT], dq[RT];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                dk[r] = dq[r] = 0.f;
+            for (int r = 0; r < RT; ++r) {                          // two sums each, of pairs: short chains
+                float2 a0 = make_float2(0.f, 0.f), a1 = a0, b0 = a0, b1 = a0;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    dk[r] = fmaf(S[r][i], k[i], dk[r]);
-                    dq[r] = fmaf(S[r][i], q[i], dq[r]);
+                for (int i = 0; i < 8; i += 2) {
+                    a0 = __ffma2_rn(S[r][i], k[i], a0);
+                    a1 = __ffma2_rn(S[r][i + 1], k[i + 1], a1);
+                    b0 = __ffma2_rn(S[r][i], q[i], b0);
+                    b1 = __ffma2_rn(S[r][i + 1], q[i + 1], b1);
                 }
+                dk[r] = (a0.x + a1.x) + (a0.y + a1.y);
+                dq[r] = (b0.x + b1.x) + (b0.y + b1.y);
             }
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                dk[r] = lane_sum<LPR>(dk[r]);
-                dq[r] = lane_sum<LPR>(dq[r]);
+            for (int r = 0; r < RT; ++r) dk[r] = lane_sum<LPR>(dk[r]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {                          // the decay needs no sum
+#pragma unroll
+                for (int i = 0; i < 8; ++i) S[r][i] = __fmul2_rn(make_float2(c.x, c.x), S[r][i]);
             }
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const float v = Io::sload(sv + t * ROWS + loc0 + r * RW);
                 const float e = c.y * (v - c.x * c.z * dk[r]) * c.z;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[r][i] = fmaf(e, k[i], c.x * S[r][i]);
-                if (qd == 0) sy[t * ROWS + loc0 + r * RW] = c.w * fmaf(e, kq, c.x * dq[r]);
+                for (int i = 0; i < 8; ++i) S[r][i] = __ffma2_rn(make_float2(e, e), k[i], S[r][i]);
+                dk[r] = e;
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                dq[r] = lane_sum<LPR>(dq[r]);
+                if (qd == 0) sy[t * ROWS + loc0 + r * RW] = c.w * fmaf(dk[r], kq, c.x * dq[r]);
             }
         }
         __syncthreads();                                            // sy complete
@@ -305,7 +325,7 @@ __global__ void __launch_bounds__(128) delta_recur_kernel(DeltaParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<float4*>(p.h_out + hoff + (size_t)r * RW * N + 4 * LPR * i) =
-                make_float4(S[r][4 * i], S[r][4 * i + 1], S[r][4 * i + 2], S[r][4 * i + 3]);
+                make_float4(S[r][2 * i].x, S[r][2 * i].y, S[r][2 * i + 1].x, S[r][2 * i + 1].y);
 }
 
 }  // namespace axon

@@ -101,13 +101,19 @@ def test_lengths(cuda_lib, L, io):
     inp = make(L=L, io=io)
     check(inp, f"L{L} {io}")
     check(inp, f"L{L} {io} no h0", h0=False)
+    if io == "bf16":
+        check(inp, f"L{L} in chunks", segments=1)
+        check(inp, f"L{L} in chunks, no h0", h0=False, segments=1)
 
 
 @pytest.mark.parametrize("N, P", [(64, 64), (64, 128), (128, 64), (128, 128)])
 @pytest.mark.parametrize("G, H", [(1, 1), (1, 3), (2, 2), (3, 12)])
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_heads(cuda_lib, N, P, G, H, io):
-    check(make(N, P, G, H, io, L=100, B=1), f"N{N} P{P} G{G} H{H} {io}")
+    inp = make(N, P, G, H, io, L=100, B=1)
+    check(inp, f"N{N} P{P} G{G} H{H} {io}")
+    if io == "bf16":
+        check(inp, f"N{N} P{P} G{G} H{H} in chunks", segments=1)
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
@@ -127,8 +133,8 @@ def test_norm_and_scale(cuda_lib, io, kw):
     check(inp, str(kw), **kw)
 
 
-@pytest.mark.parametrize("io", ["bf16", "f32"])
-def test_ragged_rows(cuda_lib, io):
+@pytest.mark.parametrize("io, segments", [("bf16", 0), ("bf16", 1), ("bf16", 3), ("f32", 0)])
+def test_ragged_rows(cuda_lib, io, segments):
     """Rows of every kind of length; what lies behind a row's end is NaN and
     infinity, and y there stays as it was."""
     lengths = [0, 1, 63, 64, 65, 130, 150, 400, -3]                 # the last two are taken into 0 .. L
@@ -139,7 +145,7 @@ def test_ragged_rows(cuda_lib, io):
         for i, name in enumerate(SEQ):
             dirty[name][b, n:] = (float("nan"), float("inf"), -float("inf"))[i % 3]
             inp[name][b, n:] = 0
-    y, h = run(dirty, lengths=lengths)
+    y, h = run(dirty, lengths=lengths, segments=segments)
     y_ref, h_ref = ref(inp, lengths=lengths)
     for b, n in enumerate(lengths):
         n = min(max(n, 0), 150)
@@ -155,10 +161,13 @@ def test_ragged_rows(cuda_lib, io):
 @pytest.mark.parametrize("L", [0, 40, 300])
 def test_state_in_place(cuda_lib, io, L):
     check(make(L=L, io=io), f"in place L{L}", in_place=True)
+    if io == "bf16" and L:
+        for segments in (1, 3):
+            check(make(L=L, io=io), f"in place L{L}, {segments} segments", in_place=True, segments=segments)
 
 
-@pytest.mark.parametrize("L", [40, 300])
-def test_slices_of_one_projection(cuda_lib, L):
+@pytest.mark.parametrize("L, segments", [(40, 0), (40, 1), (300, 0), (300, 2)])
+def test_slices_of_one_projection(cuda_lib, L, segments):
     """q, k and v as slices of one row (tokens at the row's stride), bit for
     bit what dense tensors give."""
     from selective_state_space_52_b200 import axon_ssm
@@ -169,8 +178,8 @@ def test_slices_of_one_projection(cuda_lib, L):
     q = rowed[..., 8:264].unflatten(-1, (2, 128))
     k = rowed[..., 264:520].unflatten(-1, (2, 128))
     v = rowed[..., 520:1032].unflatten(-1, (4, 128))
-    y, h = axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"])
-    y2, h2 = axon_ssm.delta_scan(q, k, v, d["dt_raw"], d["b_raw"], params, d["h0"])
+    y, h = axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"], segments=segments)
+    y2, h2 = axon_ssm.delta_scan(q, k, v, d["dt_raw"], d["b_raw"], params, d["h0"], segments=segments)
     assert torch.equal(y, y2) and torch.equal(h, h2)
 
 
@@ -191,35 +200,36 @@ def extreme(io, L=200):
     return inp
 
 
-@pytest.mark.parametrize("io", ["bf16", "f32"])
-def test_extreme_gates(cuda_lib, io):
+@pytest.mark.parametrize("io, segments", [("bf16", 0), ("bf16", 1), ("bf16", 2), ("f32", 0)])
+def test_extreme_gates(cuda_lib, io, segments):
     inp = extreme(io)
-    y, h = run(inp)
+    y, h = run(inp, segments=segments)
     y_ref, h_ref = ref(inp)
     for hd in range(4):
         close(y[:, :, hd], y_ref[:, :, hd], tols(io)[0], f"y of head {hd}", tols(io)[1])
         close(h[:, hd], h_ref[:, hd], 1e-5, f"state of head {hd}")
 
 
-@pytest.mark.parametrize("io", ["bf16", "f32"])
-def test_infinite_gates(cuda_lib, io):
+@pytest.mark.parametrize("io, segments", [("bf16", 0), ("bf16", 1), ("bf16", 2), ("f32", 0)])
+def test_infinite_gates(cuda_lib, io, segments):
     """dt_raw of +inf forgets everything, -inf nothing; b_raw likewise."""
     inp = make(io=io, L=70, B=1)
     want = {k: v.clone() for k, v in inp.items()}
     for name, t, big in (("dt_raw", 10, 3e4), ("dt_raw", 20, -3e4), ("b_raw", 30, 3e4), ("b_raw", 40, -3e4)):
         inp[name][:, t] = float("inf") if big > 0 else -float("inf")
         want[name][:, t] = big
-    y, h = run(inp)
+    y, h = run(inp, segments=segments)
     y_ref, h_ref = ref(want)
     close(y, y_ref, tols(io)[0], "y", tols(io)[1])
     close(h, h_ref, 1e-5, "state")
 
 
-def test_nan_gate_shows(cuda_lib):
+@pytest.mark.parametrize("segments", [0, 1, 2])
+def test_nan_gate_shows(cuda_lib, segments):
     """A NaN in a gate is not swallowed: its head's later outputs are NaN, the others' are not."""
     inp = make(L=90, B=1)
     inp["dt_raw"][0, 10, 1] = float("nan")
-    y, h = run(inp)
+    y, h = run(inp, segments=segments)
     assert np.isnan(y[0, 64:, 1]).all() and np.isnan(h[0, 1]).all()
     assert np.isfinite(y[0, :, [0, 2, 3]]).all() and np.isfinite(h[0, [0, 2, 3]]).all()
 
@@ -310,14 +320,15 @@ def test_outliers_in_v(cuda_lib, segments):
         close(h[:, :, v], h_ref[:, :, v], 1e-5, f"state of column {v}")
 
 
-def test_silent_stretch(cuda_lib):
+@pytest.mark.parametrize("segments", [0, 1, 3])
+def test_silent_stretch(cuda_lib, segments):
     """No values for 200 tokens: the state only decays and forgets what the keys
     touch.  A lane's numbers are kept to 2^-21 of its largest at the start of a
     chunk, and 21 chunks' worth of such errors stay below 1e-5 of the state
     before the stretch (nothing brings them up: the map never lengthens a row)."""
     inp = make(L=200, B=1)
     inp["v"][:] = 0
-    y, h = run(inp)
+    y, h = run(inp, segments=segments)
     y_ref, h_ref = ref(inp)
     assert np.abs(h - h_ref).max() <= 1e-5 * np.abs(inp["h0"].numpy()).max()
     close(y, y_ref, 2.6e-3, "y", 1.3e-2)

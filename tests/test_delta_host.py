@@ -97,7 +97,7 @@ def scan(lib, **over):
     a = dict(B=1, L=64, H=4, G=2, P=64, N=128, io=1, q=FAKE, ldq=256, k=FAKE + (1 << 24), ldk=256, v=FAKE + (2 << 24),
              ldv=256, dt_raw=FAKE + (3 << 24), b_raw=FAKE + (4 << 24), dt_bias=FAKE + (5 << 24),
              A_log=FAKE + (6 << 24), lengths=None, h0=None, scale=0.1, norm=1, y=FAKE + (7 << 24),
-             h_out=FAKE + (8 << 24), segments=0, workspace=FAKE + (9 << 24), workspace_bytes=1 << 24, stream=None)
+             h_out=FAKE + (8 << 24), segments=1, workspace=FAKE + (9 << 24), workspace_bytes=1 << 24, stream=None)
     a.update(over)
     return lib.axon_delta_scan_fwd(*a.values())
 
@@ -137,7 +137,9 @@ def test_delta_workspace_query(lib):
     state = 4 * 64 * 128 * 4
     assert q(1, 640, 4, 2, 64, 128, 1, 3) == 256 + 10 * chunk(2, 4, 128) + 2 * state + 4 * 4 * 128 * 128 + 4 * 128 * 4 + state
     assert q(1, 640, 4, 2, 128, 128, 0, 0) == 0                     # float32: token by token
-    assert q(1, 8, 4, 2, 128, 128, 1, 0) == 0                       # so are a few tokens
+    assert q(1, 8, 4, 2, 128, 128, 1, 0) == 0                       # so are a few tokens, if nothing else is asked for
+    assert q(1, 8, 4, 2, 128, 128, 1, 1) == 256 + chunk(2, 4, 128)
+    assert q(1, 1000, 4, 2, 128, 128, 1, 0) > 0
     for bad in ((-1, 64, 4, 2, 128, 128, 1, 0), (1, 64, 5, 2, 128, 128, 1, 0), (1, 64, 4, 2, 96, 128, 1, 0),
                 (1, 64, 4, 2, 128, 128, 1, -1)):
         assert q(*bad) == 0
