@@ -161,16 +161,16 @@ __device__ __forceinline__ void delta_invert(float* A, float* W, int tid) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float* row = A + (o + i) * LDA + o;
-            float acc = i == j ? 1.f : 0.f;
+            float acc[4] = {i == j ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < i; k += 4) {             // what the row holds from its diagonal on is 0
                 const float4 x4 = *reinterpret_cast<const float4*>(row + k);
-                acc = fmaf(-x4.x, t[k], acc);
-                if (k + 1 < i) acc = fmaf(-x4.y, t[k + 1], acc);
-                if (k + 2 < i) acc = fmaf(-x4.z, t[k + 2], acc);
-                if (k + 3 < i) acc = fmaf(-x4.w, t[k + 3], acc);
+                acc[0] = fmaf(-x4.x, t[k], acc[0]);
+                if (k + 1 < i) acc[1] = fmaf(-x4.y, t[k + 1], acc[1]);
+                if (k + 2 < i) acc[2] = fmaf(-x4.z, t[k + 2], acc[2]);
+                if (k + 3 < i) acc[3] = fmaf(-x4.w, t[k + 3], acc[3]);
             }
-            t[i] = acc;
+            t[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         }
         __syncwarp();
 #pragma unroll
@@ -182,7 +182,7 @@ __device__ __forceinline__ void delta_invert(float* A, float* W, int tid) {
         float* w = W + (tid >> 6) * 16 * LDW;
         float* row = A + (o + 16 + r) * LDA + o;         // of A21, then of T22 16 columns on
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+#pragma unroll 2
         for (int k = 0; k < 16; k += 4) {
             const float4 x4 = *reinterpret_cast<const float4*>(row + k);
             const float xk[4] = {x4.x, x4.y, x4.z, x4.w};
@@ -195,7 +195,7 @@ __device__ __forceinline__ void delta_invert(float* A, float* W, int tid) {
         *reinterpret_cast<float4*>(w + r * LDW + c) = s;
         __syncthreads();
         s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+#pragma unroll 2
         for (int k = 0; k < 16; k += 4) {
             const float4 x4 = *reinterpret_cast<const float4*>(row + 16 + k);
             const float xk[4] = {-x4.x, -x4.y, -x4.z, -x4.w};
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
     cp_async_wait_0();
     // each piece in place (its own thread's): the row's largest element to [1/2, 1), fp16
     unsigned char* kq = p.kq + (((size_t)b * d.G + g) * p.nC + c) * Lay::KQ_BYTES;
-#pragma unroll 1
+#pragma unroll 2
     for (int k = 0; k < 8; ++k) {
         const int t = r0 + 16 * (k & 3), s = k >> 2;
         const int in_row = (l ^ (t & 7)) << 4;
@@ -462,9 +462,15 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
             }
         }
         __syncthreads();
-        delta_invert<Lay::LDA, Lay::LDW>(A, reinterpret_cast<float*>(sm + Lay::W), tid);
         // ---- the blob: T = (I + A)^-1 diag(beta) as fp16 hi and lo tiles, M, the vectors
         unsigned char* blob = p.blob + (((size_t)b * d.H + h) * p.nC + c) * kDlBlob;
+        if (w >= 2) {                                    // beside the diagonal blocks' inversion by warps 0 and 1
+#pragma unroll
+            for (int k = 0; k < kDlTile / 16 / 64; ++k)
+                reinterpret_cast<uint4*>(blob + 2 * kDlTile)[i + 64 * k] = *reinterpret_cast<const uint4*>(sm + Lay::M + (i + 64 * k) * 16);
+            reinterpret_cast<float4*>(blob + 3 * kDlTile)[i] = reinterpret_cast<const float4*>(vec)[i];
+        }
+        delta_invert<Lay::LDA, Lay::LDW>(A, reinterpret_cast<float*>(sm + Lay::W), tid);
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
             const int row = (tid >> 3) + 16 * k, pc = tid & 7;
@@ -480,11 +486,6 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
             *reinterpret_cast<uint4*>(blob + off) = hi;
             *reinterpret_cast<uint4*>(blob + kDlTile + off) = lo;
         }
-#pragma unroll
-        for (int k = 0; k < kDlTile / 16 / 128; ++k)
-            reinterpret_cast<uint4*>(blob + 2 * kDlTile)[tid + 128 * k] =
-                *reinterpret_cast<const uint4*>(sm + Lay::M + (tid + 128 * k) * 16);
-        if (tid < kDlVec / 16) reinterpret_cast<float4*>(blob + 3 * kDlTile)[tid] = reinterpret_cast<const float4*>(vec)[tid];
         __syncthreads();
     }
     tc_fence_before();
