@@ -532,8 +532,8 @@ struct DeltaWalkSmem {
     static_assert(STAGE % 1024 == 0 && VEC % 128 == 0, "swizzled tiles and copies aligned");
     // tensor memory: the A operands hold two fp16 a column; 16 tokens of R and U_w are 8 columns hi, 8 lo
     static constexpr int S_HI = 0, S_LO = 64, DD = 0;     // the state's increment comes where S was
-    static constexpr int XK = 128, XQ = 192;              // K S^T; Q S^T, scaled, then Y
-    static constexpr int R = 256, U = 320, UW = 384, UH = 448;
+    static constexpr int XK = 128, XQ = 192;              // K S^T; Q S^T
+    static constexpr int R = 256, U = 320, UW = 384, UH = 448;    // M U comes where U was
     static constexpr int COLS = 512;
 };
 
@@ -746,9 +746,9 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 }
                 if constexpr (kFull) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)        // Y += M U
-                        umma_ts(tb + Lay::XQ + (ks >> 1) * 32, tb + Lay::UH + 8 * ks, at(k_d, Lay::M + (ks >> 1) * 4096 + ks * 32),
-                                ks < 2 ? kId64 : kId32, 1);
+                    for (int ks = 0; ks < 4; ++ks)        // M U, where U was
+                        umma_ts(tb + Lay::U + (ks >> 1) * 32, tb + Lay::UH + 8 * ks, at(k_d, Lay::M + (ks >> 1) * 4096 + ks * 32),
+                                ks < 2 ? kId64 : kId32, ks > 0);
                     umma_commit(bar(Lay::Y_M));
                 }
             }
@@ -933,14 +933,26 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 const int odd = lane & 1, t0 = (cb + c - 1) * C + 16 * part + odd, left = len - t0;
                 const size_t ystep = 2 * (size_t)d.H * P;
                 __nv_bfloat16* yo = static_cast<__nv_bfloat16*>(d.y) + (((size_t)b * d.L + t0) * d.H + h) * P + (v & ~1);
-                const float2 yl2 = make_float2(yl, yl);
-                float x[16];
-                tmem_ld16(tl + Lay::XQ + 16 * part, x);
+                // e^Gamma rq (Q S^T) + M U, times what the lane is in units of
+                const float* eq = reinterpret_cast<const float*>(sm + (st == 0 ? ST - 1 : st - 1) * Lay::STAGE + Lay::VEC) + C + 16 * part;
+                float2 yv[8];
+                {
+                    float x[16], z[16];
+                    tmem_ld16(tl + Lay::XQ + 16 * part, x);
+                    tmem_ld16(tl + Lay::U + 16 * part, z);
+#pragma unroll
+                    for (int q = 0; q < 8; q += 2) {
+                        const float4 e = *reinterpret_cast<const float4*>(eq + 2 * q);
+                        yv[q] = __ffma2_rn(make_float2(e.x, e.y), make_float2(x[2 * q], x[2 * q + 1]), make_float2(z[2 * q], z[2 * q + 1]));
+                        yv[q + 1] = __ffma2_rn(make_float2(e.z, e.w), make_float2(x[2 * q + 2], x[2 * q + 3]),
+                                               make_float2(z[2 * q + 2], z[2 * q + 3]));
+                    }
+                }
                 arrive(Lay::Y_OUT);
                 uint32_t o[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    const float2 a = __fmul2_rn(make_float2(x[2 * q], x[2 * q + 1]), yl2);
+                    const float2 a = __fmul2_rn(yv[q], make_float2(yl, yl));
                     const uint32_t mine = pack_bf16(a.x, a.y);
                     const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
                     o[q] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
@@ -999,21 +1011,6 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             // ---- U: one part for Y; weighted, two parts for the state
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                if (kFull && half == 1) {
-                    // e^Gamma rq (Q S^T), which was done before U, back to its columns while U's second half runs
-                    float x[16];
-                    uint32_t o[16];
-                    tmem_ld16(tl + Lay::XQ + 16 * part, x);
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) {
-                        const float4 e = *reinterpret_cast<const float4*>(vec + C + 16 * part + q);
-                        const float2 a = __fmul2_rn(make_float2(e.x, e.y), make_float2(x[q], x[q + 1]));
-                        const float2 f = __fmul2_rn(make_float2(e.z, e.w), make_float2(x[q + 2], x[q + 3]));
-                        o[q] = __float_as_uint(a.x); o[q + 1] = __float_as_uint(a.y);
-                        o[q + 2] = __float_as_uint(f.x); o[q + 3] = __float_as_uint(f.y);
-                    }
-                    tmem_st16(tl + Lay::XQ + 16 * part, o);
-                }
                 if (!(ok = delta_wait(bar(Lay::U_0 + half), c, dead))) break;
                 tc_fence_after();
                 const int t0 = 32 * half + 8 * part;
