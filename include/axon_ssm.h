@@ -427,7 +427,10 @@ AXON_API axon_status axon_ssd_scan_fwd(
  *   y[b,t,h,:] = scale S q^.
  * (dt is not clipped here: the erase term bounds the state, and a long memory
  * wants decays of exactly 1.  With qk_norm == 0 keys longer than
- * sqrt(2 / beta) let the state grow without bound.)
+ * sqrt(2 / beta) let the state grow without bound, and the bf16 prefill,
+ * whose products take fp16 parts, is made for keys of length near 1: longer
+ * ones than about 4 can leave fp16's range, and with all keys at length l < 1
+ * the state's relative error is some 1e-6 / l.  Queries may have any length.)
  *
  * axon_delta_scan_fwd, prefill.  Layouts: q, k (B,L,G,N) and v (B,L,H,P) io,
  * consecutive tokens ldq, ldk, ldv elements apart (ldq, ldk >= G*N, ldv >=

@@ -59,7 +59,7 @@ namespace axon {
 
 constexpr int kDlC = 64;                       // tokens per chunk
 constexpr int kDlTile = kDlC * kDlC * 2;       // a 64 x 64 fp16 tile: 8 KB
-constexpr int kDlVec = 4 * kDlC * 4;           // four rows: -ek, eq, wk, (el, y scale)
+constexpr int kDlVec = 4 * kDlC * 4;           // four rows, a value a token: -e^Gamma rk, e^Gamma, e^(Gamma_last - Gamma) rk, scale rq
 constexpr int kDlBlob = 3 * kDlTile + kDlVec;  // per chunk and value head: T hi, T lo, M, vectors
 
 struct DeltaChunkParams {
@@ -136,7 +136,7 @@ struct DeltaPrepSmem {
     static constexpr int W_END = W + 32 * LDW * 4;
     static constexpr int V = KQ_BYTES > W_END ? KQ_BYTES : W_END;   // the vectors, two heads
     static constexpr int RK = V + 2 * kDlVec;            // rk'
-    static constexpr int RQ = RK + kDlC * 4;             // rq', the largest in [1/2, 1)
+    static constexpr int RQ = RK + kDlC * 4;             // scale rq'
     static constexpr int GH = RQ + kDlC * 4;             // two heads: Gamma (log2 units), float hi and lo parts
     static constexpr int GL = GH + 2 * kDlC * 4;
     static constexpr int BE = GL + 2 * kDlC * 4;         // beta
@@ -144,8 +144,7 @@ struct DeltaPrepSmem {
     static constexpr int TOT = VJ + 2 * kDlC * 4;        // doubles: the first warps' totals
     static constexpr int MB = TOT + 16;
     static constexpr int SLOT = MB + 8;
-    static constexpr int YS = SLOT + 4;                  // scale times what RQ was divided by
-    static constexpr int BYTES = YS + 4;
+    static constexpr int BYTES = SLOT + 8;
     static constexpr int TOTAL = BYTES + 1024;           // with the alignment pad
     static_assert(M % 16 == 0 && W % 16 == 0 && V % 16 == 0 && TOT % 8 == 0, "alignment");
 };
@@ -323,7 +322,8 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
         if (l == 0) {
             // 1 / sqrt(|k|^2 + eps) in the scaled row's units: |k|^2 = ss 4^e
             const float es = pow2i(e);
-            (s ? rq : rk)[t] = d.norm ? es * rsqrtf(fmaf(ss * es, es, kDeltaEps)) : es;
+            const float f1 = d.norm ? es * rsqrtf(fmaf(ss * es, es, kDeltaEps)) : es;
+            (s ? rq : rk)[t] = s ? d.scale * f1 : f1;
         }
     }
     fence_async_smem();
@@ -340,15 +340,6 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
         umma_commit(sb + Lay::MB);
     }
     __syncwarp();
-    if (w == 3) {                                        // rq' to [1/2, 1), the rest of it to the outputs' scale
-        float m = fmaxf(rq[lane], rq[lane + 32]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int e = exp_above(m);
-        rq[lane] *= pow2i(-e);
-        rq[lane + 32] *= pow2i(-e);
-        if (lane == 0) *reinterpret_cast<float*>(sm + Lay::YS) = d.scale * pow2i(e);
-    }
     const bool ok = mbar_wait(sb + Lay::MB, 0u);
     const bool failed = __syncthreads_or(!ok);           // KQ is free from here on: A, M and W lie over it
     tc_fence_after();
@@ -403,17 +394,16 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
             float* v2 = reinterpret_cast<float*>(sm + Lay::V) + mine * 4 * C;
             reinterpret_cast<float*>(sm + Lay::VJ)[mine * C + i] = ex2_approx((gh2[r16] - hi) + (gl2[r16] - lo)) * rk[i];
             v2[i] = -eg * rk[i];
-            v2[C + i] = eg * rq[i];
+            v2[C + i] = eg;
             v2[2 * C + i] = ex2_approx((gh2[C - 1] - hi) + (gl2[C - 1] - lo)) * rk[i];
-            if (i == C - 1) v2[3 * C] = eg;
-            if (i == 0) v2[3 * C + 1] = *reinterpret_cast<const float*>(sm + Lay::YS);
+            v2[3 * C + i] = rq[i];
             __syncthreads();
         }
         // ---- row i of A, or of M.  Left of the warp's diagonal blocks of 16 the decay
         // e^(Gamma_i - Gamma_j) = e^(Gamma_i - Gamma_r) e^(Gamma_r - Gamma_j): one
         // exponential a row and block, both factors at most 1.
         const float ghi = gh[i], glo = gl[i];
-        const float f = w < 2 ? be[i] * rk[i] : rq[i];
+        const float f = w < 2 ? be[i] * rk[i] : 1.f;
         const int edge = w < 2 ? i : i + 1;              // columns below it belong to the triangle
         const int diag = 32 * (w & 1);                   // the warp's rows are diag .. diag + 31
 #pragma unroll 1
@@ -933,8 +923,8 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 const int odd = lane & 1, t0 = (cb + c - 1) * C + 16 * part + odd, left = len - t0;
                 const size_t ystep = 2 * (size_t)d.H * P;
                 __nv_bfloat16* yo = static_cast<__nv_bfloat16*>(d.y) + (((size_t)b * d.L + t0) * d.H + h) * P + (v & ~1);
-                // e^Gamma rq (Q S^T) + M U, times what the lane is in units of
-                const float* eq = reinterpret_cast<const float*>(sm + (st == 0 ? ST - 1 : st - 1) * Lay::STAGE + Lay::VEC) + C + 16 * part;
+                // scale rq (e^Gamma Q S^T + M U), times what the lane is in units of
+                const float* eg = reinterpret_cast<const float*>(sm + (st == 0 ? ST - 1 : st - 1) * Lay::STAGE + Lay::VEC) + C + 16 * part;
                 float2 yv[8];
                 {
                     float x[16], z[16];
@@ -942,10 +932,12 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                     tmem_ld16(tl + Lay::U + 16 * part, z);
 #pragma unroll
                     for (int q = 0; q < 8; q += 2) {
-                        const float4 e = *reinterpret_cast<const float4*>(eq + 2 * q);
-                        yv[q] = __ffma2_rn(make_float2(e.x, e.y), make_float2(x[2 * q], x[2 * q + 1]), make_float2(z[2 * q], z[2 * q + 1]));
-                        yv[q + 1] = __ffma2_rn(make_float2(e.z, e.w), make_float2(x[2 * q + 2], x[2 * q + 3]),
-                                               make_float2(z[2 * q + 2], z[2 * q + 3]));
+                        const float4 e = *reinterpret_cast<const float4*>(eg + 2 * q);
+                        const float4 r = *reinterpret_cast<const float4*>(eg + 2 * C + 2 * q);
+                        yv[q] = __fmul2_rn(make_float2(r.x, r.y), __ffma2_rn(make_float2(e.x, e.y), make_float2(x[2 * q], x[2 * q + 1]),
+                                                                             make_float2(z[2 * q], z[2 * q + 1])));
+                        yv[q + 1] = __fmul2_rn(make_float2(r.z, r.w), __ffma2_rn(make_float2(e.z, e.w), make_float2(x[2 * q + 2], x[2 * q + 3]),
+                                                                                 make_float2(z[2 * q + 2], z[2 * q + 3])));
                     }
                 }
                 arrive(Lay::Y_OUT);
@@ -971,7 +963,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             const unsigned short* sv = reinterpret_cast<const unsigned short*>(sg + Lay::V) + v;
             const unsigned short lamb = (unsigned short)(__float_as_uint(lam) >> 16);     // a power of two: exact
             const int rows = trans ? 0 : len - (cb + c) * C;      // tokens behind them write nothing
-            yl = ilam * vec[3 * C + 1];
+            yl = ilam;
             // ---- R = V - e^Gamma rk (K S^T), 8 tokens of each half a thread
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
@@ -1036,7 +1028,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             }
             if (!ok) break;
             // ---- the state after the chunk
-            const float el = vec[3 * C];
+            const float el = vec[2 * C - 1];              // e^Gamma of the last token
             const float2 el2 = make_float2(el, el);
             if (!(ok = N == 128 && part >= 2 ? delta_wait(bar(Lay::D_HI), c, dead) : delta_wait(bar(Lay::D), nf + c, dead))) break;
             tc_fence_after();

@@ -116,6 +116,24 @@ def test_heads(cuda_lib, N, P, G, H, io):
         check(inp, f"N{N} P{P} G{G} H{H} in chunks", segments=1)
 
 
+@pytest.mark.parametrize("segments", [0, 1, 2])
+def test_raw_keys_and_queries(cuda_lib, segments):
+    """Without the norm: keys of length 1/4 to 4 with beta |k|^2 up to 1.6, queries
+    from 1e-6 to 1e6 long within one chunk; tokens are compared each by its size."""
+    inp = make(L=200, B=1, G=2, H=4)
+    k, q = inp["k"].float(), inp["q"].float()
+    size = 4.0 ** torch.linspace(-1, 1, 200)[torch.randperm(200, generator=torch.Generator().manual_seed(3))]
+    inp["k"] = (k / k.norm(dim=-1, keepdim=True) * size[None, :, None, None]).bfloat16()
+    inp["b_raw"] = torch.full_like(inp["b_raw"], -2.2)                          # beta = 0.1
+    far = 10.0 ** (torch.arange(200) % 13 - 6)
+    inp["q"] = (q / q.norm(dim=-1, keepdim=True) * far[None, :, None, None]).bfloat16()
+    y, h = run(inp, segments=segments, qk_norm=False)
+    y_ref, h_ref = ref(inp, qk_norm=False)
+    f = far.numpy()[None, :, None, None]
+    close(y / f, y_ref / f, 2.6e-3, "y", 1.3e-2)
+    close(h, h_ref, 1e-5, "state")
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_many_blocks(cuda_lib, io):
     """Enough heads that every block keeps the most rows a lane holds."""
@@ -280,6 +298,42 @@ def test_segments_of_ragged_rows(cuda_lib, segments):
     inp = make(G=1, H=2, B=len(lengths), L=430)
     check(inp, f"{segments} segments", segments=segments, lengths=lengths)
     check(inp, f"{segments} segments in place", segments=segments, lengths=lengths, in_place=True)
+
+
+def test_no_rows_and_wrong_types(cuda_lib):
+    from selective_state_space_52_b200 import axon_ssm
+    d, params = dev(make(L=70, B=2))
+    none = [d[n][:0] for n in SEQ]
+    y, h = axon_ssm.delta_scan(*none, params)
+    assert y.shape == (0, 70, 4, 128) and h.shape == (0, 4, 128, 128)
+    assert axon_ssm.delta_step(*(t[:, 0] for t in none[:3]), *(t[:, 0].contiguous() for t in none[3:]), params,
+                               d["h0"][:0]).shape == (0, 4, 128)
+    seq = [d[n] for n in SEQ]
+    bad = [
+        (TypeError, lambda: axon_ssm.delta_scan(*(t.half() for t in seq), params)),
+        (TypeError, lambda: axon_ssm.delta_scan(seq[0].float(), *seq[1:], params)),
+        (TypeError, lambda: axon_ssm.delta_scan(*seq, params, d["h0"].bfloat16())),
+        (TypeError, lambda: axon_ssm.delta_scan(*seq, params, lengths=torch.tensor([3, 4], device="cuda"))),
+        (ValueError, lambda: axon_ssm.delta_scan(*seq, params, lengths=torch.tensor([3, 4], dtype=torch.int32))),
+        (ValueError, lambda: axon_ssm.delta_scan(seq[0][:, :-1], *seq[1:], params)),
+        (ValueError, lambda: axon_ssm.delta_scan(seq[0][..., ::2], seq[1][..., ::2], *seq[2:], params)),
+        (ValueError, lambda: axon_ssm.delta_scan(*seq[:3], seq[3].transpose(0, 1).contiguous().transpose(0, 1), seq[4], params)),
+        (ValueError, lambda: axon_ssm.delta_scan(*seq, params, d["h0"][:, :, :, ::2])),
+        (axon_ssm.AxonError, lambda: axon_ssm.delta_scan(*seq, params, segments=-1)),
+        (axon_ssm.AxonError, lambda: axon_ssm.delta_scan(*seq, params, segments=1, workspace=torch.empty(512, dtype=torch.uint8, device="cuda"))),
+        (axon_ssm.AxonError, lambda: axon_ssm.delta_scan(*seq, params, out=(d["v"], torch.empty_like(d["h0"])))),
+        (axon_ssm.AxonError, lambda: axon_ssm.delta_scan(*seq, params, scale=float("nan"))),
+        (ValueError, lambda: axon_ssm.delta_step(*(t[:, 0] for t in seq[:3]), seq[3][:, 0], seq[4][:, 0], params, d["h0"][:1])),
+        (ValueError, lambda: axon_ssm.gated_norm(d["v"], torch.ones(3, device="cuda"))),
+        (ValueError, lambda: axon_ssm.gated_norm(d["v"], z=d["v"][:1])),
+        (TypeError, lambda: axon_ssm.gated_norm(d["v"], z=d["v"].float())),
+        (axon_ssm.AxonError, lambda: axon_ssm.gated_norm(d["v"], group=96)),
+        (KeyError, lambda: axon_ssm.gated_norm(d["v"], kind="layer")),
+    ]
+    for n, (kind, call) in enumerate(bad):
+        with pytest.raises(kind):
+            call()
+            pytest.fail(f"call {n} went through")
 
 
 def test_error_flag_stays_clear(cuda_lib):
