@@ -503,7 +503,7 @@ AXON_API axon_status axon_delta_step(
  * else D values shared by the groups.  y may be x or z itself (same row
  * stride), and otherwise overlaps no input (AXON_ERR_INVALID_ARG).  D divides
  * C (AXON_ERR_INVALID_ARG) and is a multiple of 8 (bf16) or 4 (f32), as are
- * ldx, ldz, ldy (AXON_ERR_ALIGNMENT); D <= 8192 and rows * C / D < 2^31, else
+ * ldx, ldz, ldy (AXON_ERR_ALIGNMENT); D <= 8192 and rows * C / D <= 2^31 - 4096, else
  * AXON_ERR_UNSUPPORTED.  eps >= 0; a group of zeros with eps == 0 gives NaN.
  * rows == 0 is a no-op.  Float32 inside, rounded once.
  */

@@ -331,7 +331,8 @@ axon_status axon_gated_norm_fwd(int rows, int C, int D, axon_dtype io, axon_norm
     if ((io != AXON_F32 && io != AXON_BF16) || (kind != AXON_NORM_RMS && kind != AXON_NORM_GROUP) ||
         (gate != AXON_GATE_NONE && gate != AXON_GATE_AFTER && gate != AXON_GATE_BEFORE))
         return AXON_ERR_UNSUPPORTED;
-    if (D > 8192 || (long long)rows * (C / D) >= (1LL << 31)) return AXON_ERR_UNSUPPORTED;
+    // the kernel's group index runs past the last group by less than a few hundred
+    if (D > 8192 || (long long)rows * (C / D) > (1LL << 31) - 4096) return AXON_ERR_UNSUPPORTED;
     if (!(eps >= 0.0f) || !std::isfinite(eps)) return AXON_ERR_INVALID_ARG;
     if (rows == 0 || C == 0) return AXON_OK;
     const bool gated = gate != AXON_GATE_NONE;

@@ -179,7 +179,7 @@ def norm(lib, **over):
 @pytest.mark.parametrize("over, status", [
     (dict(rows=-1), 1), (dict(D=0), 1), (dict(D=-64), 1), (dict(D=96), 1), (dict(C=-256), 1), (dict(io=2), 2),
     (dict(kind=2), 2), (dict(gate=3), 2), (dict(C=16384, D=16384, ldx=16384, ldy=16384, ldz=16384), 2),
-    (dict(rows=1 << 30, D=8), 2), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
+    (dict(rows=1 << 30, D=8), 2), (dict(rows=(1 << 31) - 1, D=256), 2), (dict(rows=(1 << 29) - 1), 2), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
     (dict(x=None), 1), (dict(z=None), 1), (dict(y=None), 1), (dict(ldx=128), 1), (dict(ldz=248), 1), (dict(ldy=0), 1),
     (dict(C=260, D=4, ldx=264, ldz=264, ldy=264), 3), (dict(ldx=260), 3), (dict(x=FAKE + 2), 3), (dict(w=FAKE + (2 << 24) + 4), 3),
     (dict(y=FAKE + 512), 1), (dict(ldx=512, ldy=512, y=FAKE + 256), 1), (dict(ldx=512, ldy=512, y=FAKE + 768 + 4096), 1), (dict(y=FAKE, ldy=512), 1), (dict(y=FAKE + (1 << 24) + 1024), 1), (dict(y=FAKE + (2 << 24)), 1),
