@@ -468,7 +468,9 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * workspace overlap no input (but h_out may be h0) nor each other
  * (AXON_ERR_INVALID_ARG).  B, H <= 65535 and B*L*H <= 2^31, else
  * AXON_ERR_UNSUPPORTED.  B == 0 or H == 0 is a no-op; L == 0 copies h0 (or
- * zeros) to h_out.  Everything is float32 inside.  Other conventions as
+ * zeros) to h_out.  A NaN or infinity in a token of a row shows in its head's
+ * outputs from then on, and in chunks it may from the chunk's start.
+ * Everything is float32 inside.  Other conventions as
  * above.
  */
 AXON_API size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io, int segments);

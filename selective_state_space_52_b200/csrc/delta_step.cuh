@@ -47,7 +47,9 @@ __device__ __forceinline__ float delta_beta(float b) {
     const float r = 1.0f / (1.0f + e);
     return b >= 0.0f ? r : (b < 0.0f ? e * r : b);     // NaN stays NaN
 }
-__device__ __forceinline__ float delta_exp_a(float a_log) { return a_log >= 0.0f ? 1.0f / exp_neg(a_log) : exp_neg(-a_log); }
+__device__ __forceinline__ float delta_exp_a(float a_log) {           // exp; NaN stays NaN (exp_neg's clamp would drop it)
+    return a_log >= 0.0f ? 1.0f / exp_neg(a_log) : (a_log < 0.0f ? exp_neg(-a_log) : a_log);
+}
 
 struct DeltaParams {
     int B, L, H, G, P;

@@ -252,6 +252,23 @@ def test_nan_gate_shows(cuda_lib, segments):
     assert np.isfinite(y[0, :, [0, 2, 3]]).all() and np.isfinite(h[0, [0, 2, 3]]).all()
 
 
+@pytest.mark.parametrize("name", ["A_log", "dt_bias"])
+@pytest.mark.parametrize("segments", [0, 1, 2])
+def test_nan_parameter_shows(cuda_lib, segments, name):
+    """A NaN parameter reaches its head's outputs and state (the scan's and the step's), no other's."""
+    from selective_state_space_52_b200 import axon_ssm
+    inp = make(L=90, B=1)
+    inp[name][1] = float("nan")
+    y, h = run(inp, segments=segments)
+    assert np.isnan(y[0, 1:, 1]).all() and np.isnan(h[0, 1]).all()
+    assert np.isfinite(y[0, :, [0, 2, 3]]).all() and np.isfinite(h[0, [0, 2, 3]]).all()
+    d, params = dev(inp)
+    state = torch.ones_like(d["h0"])
+    y1 = axon_ssm.delta_step(*(d[n][:, 0] for n in SEQ[:3]), *(d[n][:, 0].contiguous() for n in SEQ[3:]), params, state)
+    assert y1[0, 1].isnan().all() and state[0, 1].isnan().all()
+    assert y1[0, [0, 2, 3]].isfinite().all() and state[0, [0, 2, 3]].isfinite().all()
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_two_calls_and_streams_agree(cuda_lib, io):
     """Back-to-back calls on one workspace, a call on another stream and a
