@@ -121,7 +121,7 @@ __device__ __forceinline__ int exp_above(float m) {
 }
 
 // ---- prep: grid = (nC, G, B), 128 threads.  What bounds it is latency and the
-// instruction caches (five blocks an SM in different phases), so the loops are
+// instruction caches (six blocks an SM in different phases), so the loops are
 // kept short: forward substitution down whole columns, unrolled over
 // registers, took 15 to 24 thousand cycles a head where this takes three.
 template <int N>
@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
     __syncwarp();
     const bool ok = mbar_wait(sb + Lay::MB, 0u);
     const bool failed = __syncthreads_or(!ok);           // KQ is free from here on: A, M and W lie over it
+    const bool drained = !failed || mbar_wait(sb + Lay::MB, 0u);
     tc_fence_after();
     if (failed && tid == 0) atomicExch(p.err, 1);
 
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == 0 && !failed) tmem_dealloc(tbase, 64);      // after a failed wait a late product might still write
+    if (w == 0 && __all_sync(0xffffffffu, drained)) tmem_dealloc(tbase, 64);   // unless a late product might still write
 }
 
 // ---- the walk: grid = (H, B, segments), 576 threads; without outputs grid =
@@ -745,13 +746,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             if (++st == ST) { st = 0; ++use; }
         }
         if (!ok) {
-            // copies and products in flight end before the block does (bounded waits)
-            if (elect_one()) {
-                atomicExch(p.err, 1);
-                umma_commit(bar(Lay::DRAIN));
-            }
-            __syncwarp();
-            mbar_wait(bar(Lay::DRAIN), 0u);
+            // copies in flight end before the block does (bounded waits); for products see the end
             for (int i = max(0, loaded - ST); i < loaded; ++i) mbar_wait(bar(Lay::FULL + i % ST), (uint32_t)(i / ST) & 1);
             for (int i = max(0, folds - 2); i < folds; ++i) mbar_wait(bar(Lay::TR_FULL + (i & 1)), (uint32_t)(i >> 1) & 1);
         }
@@ -783,7 +778,8 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
         constexpr int NQ = N / 4;                         // states of a thread: n = NQ part ..
         const uint32_t tl = tbase + ((uint32_t)(32 * (w & 3)) << 16);
         float2 S[NQ / 2];                                 // lambda times its part of the state row
-        float lam = 1.f, ilam = 1.f;                      // the lane's scale and its inverse
+        float lam = 1.f;                                  // the lane's scale, a power of two
+        auto inverse = [](float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); };   // of a power of two: exponents swapped
         const size_t hoff = (((size_t)b * d.H + h) * P + v) * N + NQ * part;
         const size_t hstep = (size_t)d.B * d.H * P * N;   // floats between segments in sloc
         const float* from = seg == 0 ? (kFull && p.h0c ? p.h0c : d.h0) : kFull ? p.sloc : nullptr;
@@ -887,7 +883,6 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                     float f = pow2i(-e);
                     if (lam * f < 0x1p-100f || lam * f > 0x1p100f) f = 1.f;    // lambda and its inverse stay floats
                     lam *= f;
-                    ilam = __uint_as_float(0x7f000000u - __float_as_uint(lam));  // of a power of two: exponents swapped
 #pragma unroll
                     for (int q = 0; q < NQ / 2; ++q) {
                         S[q] = __fmul2_rn(S[q], make_float2(f, f));
@@ -904,7 +899,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                         *reinterpret_cast<uint4*>(tile + Lay::TR_BYTES + off) =
                             make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
                     }
-                    if (part == 0) p.trs[at * N + v] = ilam;
+                    if (part == 0) p.trs[at * N + v] = inverse(lam);
                     break;
                 }
 #pragma unroll
@@ -927,17 +922,22 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 const float* eg = reinterpret_cast<const float*>(sm + (st == 0 ? ST - 1 : st - 1) * Lay::STAGE + Lay::VEC) + C + 16 * part;
                 float2 yv[8];
                 {
-                    float x[16], z[16];
-                    tmem_ld16(tl + Lay::XQ + 16 * part, x);
+                    float z[16];
                     tmem_ld16(tl + Lay::U + 16 * part, z);
 #pragma unroll
-                    for (int q = 0; q < 8; q += 2) {
-                        const float4 e = *reinterpret_cast<const float4*>(eg + 2 * q);
-                        const float4 r = *reinterpret_cast<const float4*>(eg + 2 * C + 2 * q);
-                        yv[q] = __fmul2_rn(make_float2(r.x, r.y), __ffma2_rn(make_float2(e.x, e.y), make_float2(x[2 * q], x[2 * q + 1]),
-                                                                             make_float2(z[2 * q], z[2 * q + 1])));
-                        yv[q + 1] = __fmul2_rn(make_float2(r.z, r.w), __ffma2_rn(make_float2(e.z, e.w), make_float2(x[2 * q + 2], x[2 * q + 3]),
-                                                                                 make_float2(z[2 * q + 2], z[2 * q + 3])));
+                    for (int q0 = 0; q0 < 8; q0 += 4) {
+                        float x[8];
+                        tmem_ld8(tl + Lay::XQ + 16 * part + 2 * q0, x);
+#pragma unroll
+                        for (int q = q0; q < q0 + 4; q += 2) {
+                            const float4 e = *reinterpret_cast<const float4*>(eg + 2 * q);
+                            const float4 r = *reinterpret_cast<const float4*>(eg + 2 * C + 2 * q);
+                            const float* xq = x + 2 * (q - q0);
+                            yv[q] = __fmul2_rn(make_float2(r.x, r.y), __ffma2_rn(make_float2(e.x, e.y), make_float2(xq[0], xq[1]),
+                                                                                 make_float2(z[2 * q], z[2 * q + 1])));
+                            yv[q + 1] = __fmul2_rn(make_float2(r.z, r.w), __ffma2_rn(make_float2(e.z, e.w), make_float2(xq[2], xq[3]),
+                                                                                     make_float2(z[2 * q + 2], z[2 * q + 3])));
+                        }
                     }
                 }
                 arrive(Lay::Y_OUT);
@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             const unsigned short* sv = reinterpret_cast<const unsigned short*>(sg + Lay::V) + v;
             const unsigned short lamb = (unsigned short)(__float_as_uint(lam) >> 16);     // a power of two: exact
             const int rows = trans ? 0 : len - (cb + c) * C;      // tokens behind them write nothing
-            yl = ilam;
+            yl = inverse(lam);
             // ---- R = V - e^Gamma rk (K S^T), 8 tokens of each half a thread
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
@@ -1050,6 +1050,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
         // the end state: of the segment, or, where the row ends in it, of the row
         float* to = kFull ? (cb + max(nC, 0) == all ? d.h_out : nullptr) : trans ? nullptr : p.sloc + seg * hstep;
         if (ok && to) {
+            const float ilam = inverse(lam);
 #pragma unroll
             for (int n = 0; n < NQ; n += 4)
                 *reinterpret_cast<float4*>(to + hoff + n) =
@@ -1059,7 +1060,18 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == 16 && !*dead) tmem_dealloc(tbase, Lay::COLS);   // a late product must not meet another block's columns
+    if (w == 16) {
+        bool drained = !*dead;                            // else some wait gave up, in this warp or another
+        if (!drained) {
+            if (elect_one()) {
+                atomicExch(p.err, 1);
+                umma_commit(bar(Lay::DRAIN));
+            }
+            __syncwarp();
+            drained = __all_sync(0xffffffffu, mbar_wait(bar(Lay::DRAIN), 0u));
+        }
+        if (drained) tmem_dealloc(tbase, Lay::COLS);      // a late product must not meet another block's columns
+    }
 }
 
 }  // namespace axon
