@@ -711,7 +711,7 @@ def delta_error_flag(workspace) -> int:
     """The delta rule's error flag (the workspace's first int) after the call
     that used ``workspace`` has completed.  Synchronises the device."""
     torch.cuda.synchronize(workspace.device)
-    return int(workspace[:4].view(torch.int32).item())
+    return int(workspace.view(-1).view(torch.uint8)[:4].view(torch.int32).item())
 
 
 def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, scale=None, qk_norm=True, out=None,
@@ -742,9 +742,10 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     made = _empty(stream, dev, *(((v.shape, v.dtype), (state, f32)) if out is None else ()),
                   *(((nbytes,), torch.uint8),) * (workspace is None and nbytes > 0))
     y, h_out = out if out is not None else made[:2]
-    if workspace is None and nbytes > 0:
+    given = workspace is not None
+    if not given and nbytes > 0:
         workspace = made[-1]
-    if out is not None or h0 is not None or lengths is not None:
+    if given or out is not None or h0 is not None or lengths is not None:
         _same_device("delta_scan", dev, h0=h0, lengths=lengths, y=y, h_out=h_out, workspace=workspace)
         _like("delta_scan", f32, h0=(h0, state), h_out=(h_out, state), y=(y, v.shape, v.dtype),
               lengths=(lengths, (Bsz,), torch.int32))

@@ -353,6 +353,22 @@ def test_no_rows_and_wrong_types(cuda_lib):
             pytest.fail(f"call {n} went through")
 
 
+def test_given_workspaces(cuda_lib):
+    """Of any type; on the inputs' device or refused."""
+    from selective_state_space_52_b200 import axon_ssm
+    d, params = dev(make(L=130, B=1))
+    seq = [d[n] for n in SEQ]
+    n = axon_ssm.axon_delta_workspace_bytes(1, 130, 4, 2, 128, 128, axon_ssm.AXON_BF16, 1)
+    want = axon_ssm.delta_scan(*seq, params, segments=1)
+    for dtype in (torch.uint8, torch.float32, torch.int64):
+        ws = torch.empty((2, n // 2 // dtype.itemsize), dtype=dtype, device="cuda")
+        got = axon_ssm.delta_scan(*seq, params, segments=1, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert axon_ssm.delta_error_flag(ws) == 0
+    with pytest.raises(ValueError):
+        axon_ssm.delta_scan(*seq, params, segments=1, workspace=torch.empty(n, dtype=torch.uint8))
+
+
 def test_error_flag_stays_clear(cuda_lib):
     from selective_state_space_52_b200 import axon_ssm
     d, params = dev(make(L=300, B=1))
