@@ -124,6 +124,8 @@ __device__ __forceinline__ int exp_above(float m) {
 // instruction caches (six blocks an SM in different phases), so the loops are
 // kept short: forward substitution down whole columns, unrolled over
 // registers, took 15 to 24 thousand cycles a head where this takes three.
+// 4096 tokens of 32 heads on 16 key heads, N = 128: 47 us, 43% of issue slots,
+// 62 MB from and to HBM.
 template <int N>
 struct DeltaPrepSmem {
     static constexpr int LDA = 68;                       // floats a row of A: 16-byte rows without bank conflicts
@@ -492,7 +494,9 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
 // the state row and of the tokens.  (One warp a quadrant, two blocks an SM,
 // took 12 thousand cycles a chunk: with one warp a scheduler nothing hides the
 // latencies of the conversions.)  Warp 16 copies tiles in and issues products,
-// warp 17 finds the columns' largest |v| a chunk ahead.
+// warp 17 finds the columns' largest |v| a chunk ahead.  A chunk takes 2.9 us
+// (N = P = 128): 4096 tokens of 32 heads in three segments, 69 us without and
+// 80 us with outputs, tensor pipe 28% and issue slots 53% busy.
 constexpr int kDlThreads = 576;
 constexpr int kDlStages = 3;
 

