@@ -502,3 +502,46 @@ def test_prefill_then_decode_then_norm(cuda_lib, io):
     # the norm sees y rounded to the io type, and rounds once more
     close(got, o_ref, 1e-5 if io == "f32" else 2.6e-3 + 2.3e-3, "normed output", None if io == "f32" else 4e-2)
     close(h.cpu().numpy(), h_ref, 1e-5, "state")
+
+
+@pytest.mark.parametrize("L", [20, 200])
+def test_captured_run_replays(cuda_lib, L):
+    """Prefill, norm and a step in one captured graph, replayed on other values: as eager calls."""
+    from selective_state_space_52_b200 import axon_ssm
+    a, params = dev(make(L=L, B=2))
+    b = dev(make(L=L, B=2, seed=33))[0]
+    w = torch.rand(128, device="cuda") + 0.5
+
+    def calls(d):
+        y, h = axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"], check=False)
+        o = axon_ssm.gated_norm(y.flatten(2), w, d["v"].flatten(2), group=128)
+        y1 = axon_ssm.delta_step(*(d[n][:, 3].contiguous() for n in SEQ), params, h)
+        return y, h, o, y1
+
+    want = [t.clone() for t in calls(b)]
+    graph = torch.cuda.CUDAGraph()
+    calls(a)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = calls(a)
+    for n in (*SEQ, "h0"):
+        a[n].copy_(b[n])
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("io, segments", [("bf16", 0), ("bf16", 1), ("bf16", 2), ("f32", 0)])
+def test_zero_keys_queries_and_values(cuda_lib, io, segments):
+    """Tokens whose key, query or value is 0: the norm's eps keeps them finite."""
+    inp = make(io=io, L=130, B=1)
+    inp["k"][:, 3:60:5] = 0
+    inp["q"][:, 2:130:7] = 0
+    inp["v"][:, 64:128] = 0
+    y, h = run(inp, segments=segments)
+    y_ref, h_ref = ref(inp)
+    assert (y[:, 2:130:7] == 0).all()
+    close(y, y_ref, tols(io)[0], "y", tols(io)[1])
+    close(h, h_ref, 1e-5, "state")

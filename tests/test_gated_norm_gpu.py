@@ -109,3 +109,19 @@ def test_zero_rows_and_stream(cuda_lib):
     got = axon_ssm.gated_norm(xc, wc, zc, group=128, stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("D", [64, 1920])
+def test_infinity_stays_in_its_group(cuda_lib, D):
+    """A group with a NaN or an infinity does not touch its neighbours."""
+    from selective_state_space_52_b200 import axon_ssm
+    x = torch.randn(33, 4 * D, device="cuda", generator=torch.Generator("cuda").manual_seed(5))
+    want = axon_ssm.gated_norm(x, group=D, kind="group")
+    bad = x.clone()
+    bad[3, D] = float("nan")
+    bad[32, 4 * D - 1] = float("inf")
+    got = axon_ssm.gated_norm(bad, group=D, kind="group")
+    touched = torch.zeros_like(x, dtype=torch.bool)
+    touched[3, D:2 * D] = touched[32, 3 * D:] = True
+    assert got[touched].isnan().all()
+    assert torch.equal(got[~touched], want[~touched])
