@@ -470,8 +470,10 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * AXON_ERR_UNSUPPORTED.  B == 0 or H == 0 is a no-op; L == 0 copies h0 (or
  * zeros) to h_out.  A NaN or infinity in a token of a row shows in its head's
  * outputs from then on, and in chunks it may from the chunk's start.
- * Everything is float32 inside.  Other conventions as
- * above.
+ * The state and all sums are float32.  In chunks the operands of the tensor
+ * core products are rounded further: every one but q and k (which are exact)
+ * enters as two fp16 parts, 21 significant bits of it; y is rounded once, to
+ * its io type.  Other conventions as above.
  */
 AXON_API size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io, int segments);
 

@@ -44,8 +44,9 @@
 // then exceeds 64 (1 + 64) + 64 sqrt(N) < 2^13, far inside fp16.
 // Two bf16 parts (no scale needed) came to 4.5e-6 on the final state in a
 // float64 model of these roundings, and three to half again as many products;
-// measured with fp16 parts: 5e-7.  Y takes one fp16 part of S, U and M (2^-11
-// each, below its bf16 rounding).
+// measured with fp16 parts: 5e-7.  Y's products take both parts of S, U and M
+// too, so Y is rounded once, to bf16: with the leading parts alone it was 4e-4
+// off before that, and 3.5e-4 too small (a cut part lies nearer to zero).
 #pragma once
 
 #include <cuda.h>
@@ -60,7 +61,12 @@ namespace axon {
 constexpr int kDlC = 64;                       // tokens per chunk
 constexpr int kDlTile = kDlC * kDlC * 2;       // a 64 x 64 fp16 tile: 8 KB
 constexpr int kDlVec = 4 * kDlC * 4;           // four rows, a value a token: -e^Gamma rk, e^Gamma, e^(Gamma_last - Gamma) rk, scale rq
-constexpr int kDlBlob = 3 * kDlTile + kDlVec;  // per chunk and value head: T hi, T lo, M, vectors
+// Per chunk and value head: T hi, T lo, M hi, vectors.  The three matrices are
+// lower triangular, and no product reads their upper right 32 x 32 blocks:
+// those hold the three other blocks of M lo (T hi's: rows and columns 0 .. 31,
+// T lo's: rows 32 .., columns 0 .., M hi's: rows and columns 32 ..), which as
+// a tile of their own would not fit three stages of shared memory.
+constexpr int kDlBlob = 3 * kDlTile + kDlVec;
 
 struct DeltaChunkParams {
     DeltaParams d;
@@ -410,47 +416,50 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
         const int edge = w < 2 ? i : i + 1;              // columns below it belong to the triangle
         const int diag = 32 * (w & 1);                   // the warp's rows are diag .. diag + 31
 #pragma unroll 1
-        for (int j0 = 0; j0 < C; j0 += 16) {
+        for (int j0 = 0; j0 < diag + 32; j0 += 16) {     // what is right of the diagonal blocks of 32 is not A's or M's (see kDlBlob)
             float x[16];
-            if (j0 < diag + 32) {                        // warp-uniform
-                tmem_ld16(tbase + ((uint32_t)(32 * w) << 16) + j0, x);
-                if (j0 < diag) {
-                    const float u = ex2_approx((ghi - gh[j0 + 15]) + (glo - gl[j0 + 15])) * f;
+            tmem_ld16(tbase + ((uint32_t)(32 * w) << 16) + j0, x);
+            if (j0 < diag) {
+                const float u = ex2_approx((ghi - gh[j0 + 15]) + (glo - gl[j0 + 15])) * f;
 #pragma unroll
-                    for (int q = 0; q < 16; q += 4) {
-                        const float4 v4 = *reinterpret_cast<const float4*>(vj + j0 + q);
-                        x[q] *= u * v4.x; x[q + 1] *= u * v4.y; x[q + 2] *= u * v4.z; x[q + 3] *= u * v4.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4) {
-                        const float4 h4 = *reinterpret_cast<const float4*>(gh + j0 + q);
-                        const float4 l4 = *reinterpret_cast<const float4*>(gl + j0 + q);
-                        const float4 r4 = *reinterpret_cast<const float4*>(rk + j0 + q);
-                        const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
-                        const float rj[4] = {r4.x, r4.y, r4.z, r4.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float dec = ex2_approx((ghi - hj[e]) + (glo - lj[e]));
-                            x[q + e] = j0 + q + e < edge ? x[q + e] * f * (dec * rj[e]) : 0.f;
-                        }
-                    }
+                for (int q = 0; q < 16; q += 4) {
+                    const float4 v4 = *reinterpret_cast<const float4*>(vj + j0 + q);
+                    x[q] *= u * v4.x; x[q + 1] *= u * v4.y; x[q + 2] *= u * v4.z; x[q + 3] *= u * v4.w;
                 }
             } else {
 #pragma unroll
-                for (int q = 0; q < 16; ++q) x[q] = 0.f;
+                for (int q = 0; q < 16; q += 4) {
+                    const float4 h4 = *reinterpret_cast<const float4*>(gh + j0 + q);
+                    const float4 l4 = *reinterpret_cast<const float4*>(gl + j0 + q);
+                    const float4 r4 = *reinterpret_cast<const float4*>(rk + j0 + q);
+                    const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
+                    const float rj[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float dec = ex2_approx((ghi - hj[e]) + (glo - lj[e]));
+                        x[q + e] = j0 + q + e < edge ? x[q + e] * f * (dec * rj[e]) : 0.f;
+                    }
+                }
             }
             if (w < 2) {
 #pragma unroll
                 for (int q = 0; q < 16; q += 4)
                     *reinterpret_cast<float4*>(A + i * Lay::LDA + j0 + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
             } else {
+                // M lo: the block at (32, 32) into M's tile, the others beside A's
+                // rows 0 .. 31 (bytes 128 .. of a row: M's rows 0 .., then 32 ..), on their way to T's tiles
+                const int il = i & 31;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int pc = j0 / 8 + q;
-                    *reinterpret_cast<uint4*>(sm + Lay::M + i * 128 + ((pc ^ (i & 7)) << 4)) =
-                        make_uint4(pack_f16(x[8 * q], x[8 * q + 1]), pack_f16(x[8 * q + 2], x[8 * q + 3]),
-                                   pack_f16(x[8 * q + 4], x[8 * q + 5]), pack_f16(x[8 * q + 6], x[8 * q + 7]));
+                    uint4 hi, lo;
+                    split_f16(make_float2(x[8 * q], x[8 * q + 1]), hi.x, lo.x);
+                    split_f16(make_float2(x[8 * q + 2], x[8 * q + 3]), hi.y, lo.y);
+                    split_f16(make_float2(x[8 * q + 4], x[8 * q + 5]), hi.z, lo.z);
+                    split_f16(make_float2(x[8 * q + 6], x[8 * q + 7]), hi.w, lo.w);
+                    *reinterpret_cast<uint4*>(sm + Lay::M + i * 128 + ((pc ^ (i & 7)) << 4)) = hi;
+                    *reinterpret_cast<uint4*>(pc >= 4 ? sm + Lay::M + il * 128 + ((pc ^ (il & 7)) << 4)
+                                                      : sm + Lay::A + il * (Lay::LDA * 4) + 128 + 2 * diag + 16 * pc) = lo;
                 }
             }
         }
@@ -475,6 +484,10 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
             split_f16(make_float2(a0.z * b0.z, a0.w * b0.w), hi.y, lo.y);
             split_f16(make_float2(a1.x * b1.x, a1.y * b1.y), hi.z, lo.z);
             split_f16(make_float2(a1.z * b1.z, a1.w * b1.w), hi.w, lo.w);
+            if (k < 2 && pc >= 4) {                      // M lo's blocks
+                hi = *reinterpret_cast<const uint4*>(sm + Lay::A + row * (Lay::LDA * 4) + 64 + 16 * pc);
+                lo = *reinterpret_cast<const uint4*>(sm + Lay::A + row * (Lay::LDA * 4) + 128 + 16 * pc);
+            }
             const int off = row * 128 + ((pc ^ (row & 7)) << 4);
             *reinterpret_cast<uint4*>(blob + off) = hi;
             *reinterpret_cast<uint4*>(blob + kDlTile + off) = lo;
@@ -525,7 +538,7 @@ struct DeltaWalkSmem {
     static_assert(2 * TR_BYTES <= STAGE, "a transition fits a stage");
     static_assert(TOTAL <= 227 * 1024, "shared memory of a block");
     static_assert(STAGE % 1024 == 0 && VEC % 128 == 0, "swizzled tiles and copies aligned");
-    // tensor memory: the A operands hold two fp16 a column; 16 tokens of R and U_w are 8 columns hi, 8 lo
+    // tensor memory: the A operands hold two fp16 a column; 16 tokens of R, U_w and U (for Y) are 8 columns hi, 8 lo
     static constexpr int S_HI = 0, S_LO = 64, DD = 0;     // the state's increment comes where S was
     static constexpr int XK = 128, XQ = 192;              // K S^T; Q S^T
     static constexpr int R = 256, U = 320, UW = 384, UH = 448;    // M U comes where U was
@@ -684,10 +697,11 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             if constexpr (kFull) {
                 if (!(ok = c == 0 || delta_wait(bar(Lay::Y_OUT), c - 1, dead))) break;
                 tc_fence_after();
-                if (elect_one()) {                            // Q S^T, the hi part
+                if (elect_one()) {                            // Q S^T, both parts of S
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-                        umma_ts(tb + Lay::XQ, tb + Lay::S_HI + 8 * ks, at(k_d, Lay::Q + rows(ks)), kId64, ks > 0);
+                    for (int ks = 0; ks < 2 * KS; ++ks)
+                        umma_ts(tb + Lay::XQ, tb + (ks / KS) * Lay::S_LO + 8 * (ks % KS), at(k_d, Lay::Q + rows(ks % KS)),
+                                kId64, ks > 0);
                     umma_commit(bar(Lay::X_Q));
                 }
             }
@@ -740,10 +754,19 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                     umma_commit(bar(Lay::D_HI));
                 }
                 if constexpr (kFull) {
+                    // M U, where U was: hi hi and hi lo (U lo), then lo hi from where M lo's blocks lie
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)        // M U, where U was
-                        umma_ts(tb + Lay::U + (ks >> 1) * 32, tb + Lay::UH + 8 * ks, at(k_d, Lay::M + (ks >> 1) * 4096 + ks * 32),
-                                ks < 2 ? kId64 : kId32, ks > 0);
+                    for (int k2 = 0; k2 < 8; ++k2) {
+                        const int ks = k2 & 3;
+                        umma_ts(tb + Lay::U + (ks >> 1) * 32, tb + Lay::UH + 16 * ks + 8 * (k2 >> 2),
+                                at(k_d, Lay::M + (ks >> 1) * 4096 + ks * 32), ks < 2 ? kId64 : kId32, k2 > 0);
+                    }
+#pragma unroll
+                    for (int k2 = 0; k2 < 6; ++k2) {
+                        const int blk = k2 >> 1, q = k2 & 1;          // (0, 0), (32, 0), (32, 32)
+                        umma_ts(tb + Lay::U + (blk > 0) * 32, tb + Lay::UH + 16 * (2 * (blk >> 1) + q),
+                                at(k_d, (blk == 2 ? Lay::M : Lay::T + blk * kDlTile) + 64 + q * 32), kId32, 1);
+                    }
                     umma_commit(bar(Lay::Y_M));
                 }
             }
@@ -1004,7 +1027,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 arrive(Lay::R_IN0 + half);
             }
             if (!ok) break;
-            // ---- U: one part for Y; weighted, two parts for the state
+            // ---- U for Y, and weighted for the state
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 if (!(ok = delta_wait(bar(Lay::U_0 + half), c, dead))) break;
@@ -1012,11 +1035,13 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                 const int t0 = 32 * half + 8 * part;
                 float x[8];
                 tmem_ld8(tl + Lay::U + t0, x);
-                uint32_t u[4], hi[4], lo[4];
+                uint32_t hi[4], lo[4];
+                const uint32_t to = 32 * half + 16 * (part >> 1) + 4 * (part & 1);
                 if constexpr (kFull) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) u[q] = pack_f16(x[2 * q], x[2 * q + 1]);
-                    tmem_st4(tl + Lay::UH + t0 / 2, u);
+                    for (int q = 0; q < 4; ++q) split_f16(make_float2(x[2 * q], x[2 * q + 1]), hi[q], lo[q]);
+                    tmem_st4(tl + Lay::UH + to, hi);
+                    tmem_st4(tl + Lay::UH + to + 8, lo);
                 }
 #pragma unroll
                 for (int q = 0; q < 4; q += 2) {
@@ -1024,9 +1049,8 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                     split_f16(__fmul2_rn(make_float2(x[2 * q], x[2 * q + 1]), make_float2(wk.x, wk.y)), hi[q], lo[q]);
                     split_f16(__fmul2_rn(make_float2(x[2 * q + 2], x[2 * q + 3]), make_float2(wk.z, wk.w)), hi[q + 1], lo[q + 1]);
                 }
-                const uint32_t r = tl + Lay::UW + 32 * half + 16 * (part >> 1) + 4 * (part & 1);
-                tmem_st4(r, hi);
-                tmem_st4(r + 8, lo);
+                tmem_st4(tl + Lay::UW + to, hi);
+                tmem_st4(tl + Lay::UW + to + 8, lo);
                 tmem_st_wait();
                 arrive(Lay::U_IN0 + half);
             }
