@@ -680,10 +680,14 @@ def _all_as(dtype, index, *tensors):
     return True
 
 
-def _delta_args(what, q, k, v, dt_raw, b_raw, params):
+def _delta_args(what, lead_dims, q, k, v, dt_raw, b_raw, params):
     """Sizes and pointer arguments, checked (small calls are bound by this code:
-    the common case is looked over in one go, the rest explains itself)."""
+    the common case is looked over in one go, the rest explains itself).
+    ``lead_dims``: dimensions before the heads, (B, L) or (B,); with others the
+    sizes below would be read off the wrong ones."""
     bias, a_log = params["dt_bias"], params["A_log"]
+    if v.dim() != lead_dims + 2:
+        raise ValueError(f"{what}: v has {v.dim()} dimensions, not {lead_dims + 2}")
     dt, i = v.dtype, v.get_device()
     *lead, H, P = v.shape
     G, N = k.shape[-2:]
@@ -730,7 +734,7 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     (AXON_ERR_TIMEOUT) if a wait of the kernel gave up; ``check=False`` returns
     at once (read the flag with ``delta_error_flag(workspace)``).
     """
-    i, H, P, G, N, io, args = _delta_args("delta_scan", q, k, v, dt_raw, b_raw, params)
+    i, H, P, G, N, io, args = _delta_args("delta_scan", 2, q, k, v, dt_raw, b_raw, params)
     if i != _current_device():
         with torch.cuda.device(i):
             return delta_scan(q, k, v, dt_raw, b_raw, params, h0, lengths=lengths, scale=scale, qk_norm=qk_norm,
@@ -762,7 +766,7 @@ def delta_step(q, k, v, dt_raw, b_raw, params: dict, state, *, scale=None, qk_no
     """One cached step of the gated delta rule: q, k (B,G,N), v (B,H,P),
     dt_raw, b_raw (B,H); ``state`` (B,H,P,N) float32 is updated in place.
     Returns y (B,H,P)."""
-    i, H, P, G, N, io, args = _delta_args("delta_step", q, k, v, dt_raw, b_raw, params)
+    i, H, P, G, N, io, args = _delta_args("delta_step", 1, q, k, v, dt_raw, b_raw, params)
     if i != _current_device():
         with torch.cuda.device(i):
             return delta_step(q, k, v, dt_raw, b_raw, params, state, scale=scale, qk_norm=qk_norm, y=y, stream=stream)

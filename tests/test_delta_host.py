@@ -224,3 +224,65 @@ def test_binding_token_strides(lib):
         _row_stride("f", "t", row[:, :4, :128], 8, 128)
     with pytest.raises(ValueError):
         _row_stride("f", "t", row[..., ::2], 10, 320)
+
+
+@pytest.fixture
+def recorded(lib, monkeypatch):
+    """The binding on CPU tensors with a recorder in place of the library: what would be launched, launched nowhere."""
+    from selective_state_space_52_b200 import axon_ssm
+    calls = []
+
+    class Recorder:
+        def __getattr__(self, name):
+            def call(*args):
+                calls.append((name, args))
+                return 0
+            return call
+
+    monkeypatch.setattr(axon_ssm, "_lib", Recorder())
+    monkeypatch.setattr(axon_ssm, "_same_device", lambda what, dev, **tensors: None)
+    monkeypatch.setattr(axon_ssm, "_current_device", lambda: -1)
+    monkeypatch.setattr(axon_ssm, "_stream_on", lambda stream, index: None)
+    return axon_ssm, calls
+
+
+def delta_tensors(*lead, G=2, H=4, P=64, N=64):
+    def t(*shape):
+        return torch.zeros(*lead, *shape, dtype=torch.bfloat16)
+    params = {"dt_bias": torch.zeros(H), "A_log": torch.zeros(H)}
+    return t(G, N), t(G, N), t(H, P), t(H), t(H), params
+
+
+@pytest.mark.parametrize("lead", [(), (4,), (2, 3, 5), (1, 2, 3, 5)])
+def test_delta_scan_refuses_other_ranks(recorded, lead):
+    """A step's tensors or a prompt without its batch dimension would pass heads for tokens."""
+    axon_ssm, calls = recorded
+    with pytest.raises(ValueError, match="dimensions"):
+        axon_ssm.delta_scan(*delta_tensors(*lead))
+    assert not calls
+
+
+@pytest.mark.parametrize("lead", [(), (2, 1), (2, 3), (2, 3, 5)])
+def test_delta_step_refuses_other_ranks(recorded, lead):
+    axon_ssm, calls = recorded
+    with pytest.raises(ValueError, match="dimensions"):
+        axon_ssm.delta_step(*delta_tensors(*lead), torch.zeros(2, 4, 64, 64))
+    assert not calls
+
+
+@pytest.mark.parametrize("which", [0, 1, 2, 3, 4])
+def test_delta_refuses_one_tensor_of_another_rank(recorded, which):
+    axon_ssm, calls = recorded
+    args = list(delta_tensors(2, 8))
+    for bad in (args[which][0], args[which][None], args[which].flatten()[0]):
+        with pytest.raises(ValueError):
+            axon_ssm.delta_scan(*args[:which], bad, *args[which + 1:])
+    assert not calls
+
+
+def test_delta_right_ranks_reach_the_library(recorded):
+    axon_ssm, calls = recorded
+    axon_ssm.delta_scan(*delta_tensors(2, 8), check=False)
+    axon_ssm.delta_step(*delta_tensors(3), torch.zeros(3, 4, 64, 64))
+    scan_args, step_args = (a for n, a in calls if n != "axon_delta_workspace_bytes")
+    assert scan_args[:6] == (2, 8, 4, 2, 64, 64) and step_args[:5] == (3, 4, 2, 64, 64)
