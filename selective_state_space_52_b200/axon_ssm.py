@@ -631,6 +631,15 @@ def _like(what, dtype, **tensors):
             raise TypeError(f"{what}: {name} is {t.dtype}, not {want}")
 
 
+_INT_MAX = 2 ** 31 - 1         # of a count or stride: ctypes would keep the low 32 bits of more without a word
+
+
+def _stride_fits(what, name, ld):
+    if ld > _INT_MAX:
+        raise ValueError(f"{what}: the stride of {name} is {ld} elements, more than 2^31 - 1")
+    return ld
+
+
 def _token_stride(what, name, t):
     """Elements between consecutive tokens of a (B, L, heads, D) or (B, heads,
     D) tensor whose heads are dense and whose tokens lie at one stride (a slice
@@ -646,7 +655,7 @@ def _token_stride(what, name, t):
             n *= t.shape[i]
     if (d > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != d):
         raise ValueError(f"{what}: the heads of {name} must be dense")
-    return ld
+    return _stride_fits(what, name, ld)
 
 
 def _empty(stream, dev, *specs):
@@ -804,7 +813,7 @@ def _row_stride(what, name, t, rows, C):
         ld = t2.stride(0) if rows > 1 else C
     if C > 1 and t.stride(-1) != 1:
         raise ValueError(f"{what}: the channels of {name} must be dense")
-    return ld
+    return _stride_fits(what, name, ld)
 
 
 def gated_norm(x, weight=None, z=None, *, bias=None, group=None, kind="rms", gate="after", act=True, eps=1e-6,
@@ -832,6 +841,8 @@ def gated_norm(x, weight=None, z=None, *, bias=None, group=None, kind="rms", gat
     if n != D and n != C:
         raise ValueError(f"gated_norm: weight and bias need {D} or {C} values, not {n}")
     rows = x.numel() // C if C else 0
+    if rows > _INT_MAX or C > _INT_MAX or D > _INT_MAX:
+        raise AxonError(2, "axon_gated_norm_fwd")
     params = [t for t in (weight, bias) if t is not None]
     data = [x, y] if z is None else [x, y, z]
     if (_all_as(torch.float32, i, *params) and all(t.shape == (n,) for t in params) and _all_as(x.dtype, i, *data) and

@@ -286,3 +286,46 @@ def test_delta_right_ranks_reach_the_library(recorded):
     axon_ssm.delta_step(*delta_tensors(3), torch.zeros(3, 4, 64, 64))
     scan_args, step_args = (a for n, a in calls if n != "axon_delta_workspace_bytes")
     assert scan_args[:6] == (2, 8, 4, 2, 64, 64) and step_args[:5] == (3, 4, 2, 64, 64)
+
+
+# ------------------------------------------------------------ counts and strides that the C ABI's ints cannot hold
+@pytest.mark.parametrize("shape, group", [(((1 << 32) + 5, 8), None), ((1 << 31, 8), None), ((1 << 16, 1 << 15, 16), 8),
+                                          ((1, (1 << 32) + 64), None), ((1, (1 << 32) + 64), 64), ((3, 128), (1 << 32) + 64)])
+def test_gated_norm_refuses_counts_past_31_bits(recorded, shape, group):
+    """Only the low 32 bits would reach the library: 2^32 + 5 rows as 5."""
+    axon_ssm, calls = recorded
+    x = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(axon_ssm.AxonError) as e:
+        axon_ssm.gated_norm(x, group=group, out=x)
+    assert e.value.status == 2 and not calls
+
+
+def far_apart(stride, *tail):
+    """Two rows (or one token of two batch rows) `stride` elements apart; no memory behind them."""
+    return torch.empty(2 * stride, dtype=torch.bfloat16, device="meta").as_strided((2, *tail), (stride, *torch.empty(tail, device="meta").stride()))
+
+
+@pytest.mark.parametrize("stride", [1 << 31, (1 << 32) + 128, (1 << 32) + 4096])
+def test_strides_past_31_bits_are_refused(recorded, stride):
+    axon_ssm, calls = recorded
+    wide, x = far_apart(stride, 128), torch.empty(2, 128, dtype=torch.bfloat16, device="meta")
+    for kw in (dict(x=wide, out=x), dict(x=x, z=wide, out=x), dict(x=x, out=wide)):
+        with pytest.raises(ValueError, match="stride"):
+            axon_ssm.gated_norm(group=64, **kw)
+    q, k, v, dt_raw, b_raw, params = (t if isinstance(t, dict) else t.to("meta") for t in delta_tensors(2))
+    state = torch.empty(2, 4, 64, 64, device="meta")
+    for n, t in enumerate((far_apart(stride, 2, 64), far_apart(stride, 2, 64), far_apart(stride, 4, 64))):
+        args = [q, k, v]
+        args[n] = t
+        with pytest.raises(ValueError, match="stride"):
+            axon_ssm.delta_step(*args, dt_raw, b_raw, params, state)
+        with pytest.raises(ValueError, match="stride"):
+            axon_ssm.delta_scan(*(u[:, None] for u in (*args, dt_raw, b_raw)), params, check=False)
+    assert not calls
+
+
+def test_the_largest_stride_passes(lib):
+    from selective_state_space_52_b200.axon_ssm import _row_stride, _token_stride
+    last = (1 << 31) - 8
+    assert _row_stride("f", "t", far_apart(last, 128), 2, 128) == last
+    assert _token_stride("f", "t", far_apart(last, 2, 64)) == last
