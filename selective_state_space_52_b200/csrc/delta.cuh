@@ -119,12 +119,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }    // -126 <= e <= 127
 
-// Rows' largest magnitude m > 0: the exponent e with m 2^-e in [1/2, 1),
-// held to what a float power of two and its inverse can say.
-__device__ __forceinline__ int exp_above(float m) {
-    const int e = (int)((__float_as_uint(m) >> 23) & 255u) - 126;
-    return min(max(e, -100), 100);
-}
+// For m > 0 the exponent e with m 2^-e in [1/2, 1); ..
+__device__ __forceinline__ int exp_of(float m) { return (int)((__float_as_uint(m) >> 23) & 255u) - 126; }
+// .. held to what a float power of two and its inverse can say (m 2^-e < 4).
+__device__ __forceinline__ int exp_above(float m) { return min(max(exp_of(m), -126), 126); }
 
 // ---- prep: grid = (nC, G, B), 128 threads.  What bounds it is latency and the
 // instruction caches (six blocks an SM in different phases), so the loops are
@@ -890,32 +888,38 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             const unsigned char* sg = sm + st * Lay::STAGE;
             if (c < nC || trans) {
                 // ---- the lane's scale for this chunk, S into the A operand's columns:
-                // first in the scale it has, which nearly always stands
+                // first in the scale it has, which mostly stands, else once more
                 float m;
                 lane_max(S, m);
                 uint32_t hi[NQ / 2], lo[NQ / 2];
+#pragma unroll 1
+                for (bool again = false;; again = true) {
 #pragma unroll
-                for (int q = 0; q < NQ / 2; ++q) split_f16(S[q], hi[q], lo[q]);
-                // every thread of the lane has read its increment too; V and the vectors are here
-                if (!(ok = lane_max_wait(nf + c, m))) break;
-                if (trans) {
-                    if (c < nC && !(ok = delta_wait(bar(Lay::FULL + st), use, dead))) break;
-                } else {
-                    if (!(ok = delta_wait(bar(Lay::VMAX + st), use, dead))) break;
-                    m = fmaxf(m, lam * reinterpret_cast<const float*>(sm + Lay::VM)[st * P + v]);
-                }
-                const bool out = m > 64.f || (m < 0.125f && m > 0.f);
-                if (__any_sync(0xffffffffu, out)) {
-                    const int e = out ? exp_above(m) : 0;
-                    float f = pow2i(-e);
-                    if (lam * f < 0x1p-100f || lam * f > 0x1p100f) f = 1.f;    // lambda and its inverse stay floats
-                    lam *= f;
-#pragma unroll
-                    for (int q = 0; q < NQ / 2; ++q) {
-                        S[q] = __fmul2_rn(S[q], make_float2(f, f));
-                        split_f16(S[q], hi[q], lo[q]);
+                    for (int q = 0; q < NQ / 2; ++q) split_f16(S[q], hi[q], lo[q]);
+                    if (again) break;
+                    // every thread of the lane has read its increment too; V and the vectors are here
+                    if (!(ok = lane_max_wait(nf + c, m))) break;
+                    float vm = 0.f;
+                    if (trans) {
+                        if (c < nC && !(ok = delta_wait(bar(Lay::FULL + st), use, dead))) break;
+                    } else {
+                        if (!(ok = delta_wait(bar(Lay::VMAX + st), use, dead))) break;
+                        vm = reinterpret_cast<const float*>(sm + Lay::VM)[st * P + v];
                     }
+                    const float both = fmaxf(m, lam * vm);    // infinite or 0 where the product leaves float's range
+                    const bool out = both > 64.f || (both < 0.125f && (m > 0.f || vm > 0.f));
+                    if (!__any_sync(0xffffffffu, out)) break;
+                    const int l = exp_of(lam) - 1;            // by exponents, which stay in range
+                    int e = 0;
+                    if (out) e = max(m > 0.f ? exp_of(m) : -1000, vm > 0.f ? exp_of(vm) + l : -1000);
+                    e = min(max(e, l - 126), l + 126);        // lambda and its inverse stay floats
+                    lam = pow2i(l - e);
+                    // beyond 2^126 S is 0 (up), or nothing beside V (down: below 2^-120 of it)
+                    const float f = pow2i(-min(max(e, -126), 126));
+#pragma unroll
+                    for (int q = 0; q < NQ / 2; ++q) S[q] = __fmul2_rn(S[q], make_float2(f, f));
                 }
+                if (!ok) break;
                 if (!kFull && c == nC) {                  // the segment's transition: row v, this thread's columns
                     const size_t at = ((size_t)(seg - 1) * d.B + b) * d.H + h;
                     unsigned char* tile = p.tr + at * 2 * Lay::TR_BYTES + (NQ * part / 64) * (N * 128) + v * 128;

@@ -572,3 +572,56 @@ def test_y_is_rounded_once(cuda_lib, N, P, segments):
     slope = np.sum(y * y_ref) / s2
     noise = 2 ** -8 / np.sqrt(3) * np.sqrt(np.sum(y_ref ** 4)) / s2
     assert abs(slope - 1) <= 6 * noise + 2 ** -17, (slope - 1, noise)
+
+
+# ------------------------------------------------------------ values anywhere in float32's range
+@pytest.mark.parametrize("segments", [1, 3])
+@pytest.mark.parametrize("power", [-110, -90, 90, 115])
+def test_values_near_the_types_limits(cuda_lib, power, segments):
+    """As test_scaled_values, up to where a state of some 2^8 times the values is still finite
+    (and down to where few of its elements leave the normal range)."""
+    inp = make(L=300, B=1)
+    inp["v"] = (inp["v"].double() * 2.0 ** power).bfloat16()
+    inp["h0"] = (inp["h0"].double() * 2.0 ** power).float()
+    y, h = run(inp, segments=segments)
+    y_ref, h_ref = ref(inp)
+    close(y / 2.0 ** power, y_ref / 2.0 ** power, 2.6e-3, "y", 1.3e-2)
+    close(h / 2.0 ** power, h_ref / 2.0 ** power, 1e-5, "state")
+
+
+@pytest.mark.parametrize("segments", [0, 1, 3])
+@pytest.mark.parametrize("first, then", [(-70, 70), (-110, 20), (0, 110), (110, -5), (70, -70)])
+def test_values_jump(cuda_lib, first, then, segments):
+    """Values of one size, then, from a chunk on, of another: up by 2^110 or 2^140 at once,
+    or down, after a decay that leaves nothing of the first."""
+    inp = make(L=330, B=1)
+    v = inp["v"].double()
+    v[:, :192] *= 2.0 ** first
+    v[:, 192:] *= 2.0 ** then
+    inp["h0"] = inp["h0"] * 0
+    if first > then:
+        v[:, 150:192] = 0
+        inp["dt_raw"][:, 150:160] = 60.0             # e^-60 at most, at each of ten tokens
+    inp["v"] = v.bfloat16()
+    y, h = run(inp, segments=segments)
+    y_ref, h_ref = ref(inp)
+    for a, b, p in ((0, 192, first), (192, 330, then)):
+        close(y[:, a:b] / 2.0 ** p, y_ref[:, a:b] / 2.0 ** p, 2.6e-3, f"y of tokens {a} to {b}", 1.3e-2)
+    close(h / 2.0 ** then, h_ref / 2.0 ** then, 1e-5, "state")
+
+
+@pytest.mark.parametrize("segments", [0, 1, 2])
+@pytest.mark.parametrize("power", [-110, 110, 118])
+def test_raw_queries_of_any_length(cuda_lib, power, segments):
+    """Without the norm: queries 2^power long, values that bring y back to normal size."""
+    inp = make(L=200, B=1)
+    k, q = inp["k"].float(), inp["q"].double()
+    inp["k"] = (k / k.norm(dim=-1, keepdim=True)).bfloat16()
+    inp["q"] = (q / q.norm(dim=-1, keepdim=True) * 2.0 ** power).bfloat16()
+    inp["v"] = (inp["v"].double() * 2.0 ** (-power // 2)).bfloat16()
+    inp["h0"] = (inp["h0"].double() * 2.0 ** (-power // 2)).float()
+    y, h = run(inp, segments=segments, qk_norm=False)
+    y_ref, h_ref = ref(inp, qk_norm=False)
+    p = 2.0 ** (power - power // 2)
+    close(y / p, y_ref / p, 2.6e-3, "y", 1.3e-2)
+    close(h / 2.0 ** (-power // 2), h_ref / 2.0 ** (-power // 2), 1e-5, "state")
