@@ -427,10 +427,14 @@ AXON_API axon_status axon_ssd_scan_fwd(
  *   y[b,t,h,:] = scale S q^.
  * (dt is not clipped here: the erase term bounds the state, and a long memory
  * wants decays of exactly 1.  With qk_norm == 0 keys longer than
- * sqrt(2 / beta) let the state grow without bound, and the bf16 prefill,
- * whose products take fp16 parts, is made for keys of length near 1: longer
- * ones than about 4 can leave fp16's range, and with all keys at length l < 1
- * the state's relative error is some 1e-6 / l.  Queries may have any length.)
+ * sqrt(2 / beta) let the state grow without bound, and bf16 prefill in chunks,
+ * whose products take fp16 parts, is made for keys of length near 1: with
+ * longer ones than about 4 an operand can leave fp16's range, which shows as
+ * infinity or NaN and in the error flag; with all keys at length l < 1 the state's relative error
+ * is some 1e-6 / l.  Queries may have any length.  In chunks a value column
+ * of 64 tokens and the state before them keep 21 bits of their largest value:
+ * what is smaller by more than that, in the same chunk, is lost.  Token by
+ * token neither limit holds.)
  *
  * axon_delta_scan_fwd, prefill.  Layouts: q, k (B,L,G,N) and v (B,L,H,P) io,
  * consecutive tokens ldq, ldk, ldv elements apart (ldq, ldk >= G*N, ldv >=
@@ -459,9 +463,11 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * `workspace` (16-byte aligned; may be NULL when the size is 0) holds
  * axon_delta_workspace_bytes(B, L, H, G, P, N, io, segments) bytes for the
  * same `segments` on the current device.  Where it is used, its first 4 bytes
- * (an int) are an error flag, cleared by each call and set to 1 if a wait of a
- * kernel for its copies or products gave up (the outputs are then undefined);
- * read it after the call completes.  Every call writes what it reads in the
+ * (an int) are an error flag, cleared by each call: bit 0 is set if a wait of
+ * a kernel for its copies or products gave up (the outputs are then undefined),
+ * bit 1 if, with qk_norm == 0, y or the end state is not finite: an operand
+ * left fp16's range, or an input was not finite.  Read it after the call
+ * completes.  Every call writes what it reads in the
  * workspace, so calls that may run at the same time (streams, captured graphs)
  * need one each.  Pointers 16-byte aligned and ldq, ldk, ldv
  * multiples of 8 (bf16) or 4 (f32), else AXON_ERR_ALIGNMENT; y, h_out and the

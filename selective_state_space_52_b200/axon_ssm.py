@@ -722,9 +722,22 @@ def _delta_args(what, lead_dims, q, k, v, dt_raw, b_raw, params):
 
 def delta_error_flag(workspace) -> int:
     """The delta rule's error flag (the workspace's first int) after the call
-    that used ``workspace`` has completed.  Synchronises the device."""
+    that used ``workspace`` has completed: bit 0 a wait gave up, bit 1 with raw
+    keys y or the state is not finite.  Synchronises the device."""
     torch.cuda.synchronize(workspace.device)
     return int(workspace.view(-1).view(torch.uint8)[:4].view(torch.int32).item())
+
+
+def _finite_tokens(lengths, values, gates, params, h0) -> bool:
+    """Whether the rows' tokens, the parameters and the state are numbers (a gate may be infinite)."""
+    L = values[0].shape[1]
+    behind = None if lengths is None else torch.arange(L, device=lengths.device) >= lengths[:, None]
+    for t in (*values, *gates):
+        bad = t.isnan() if t.dim() == 3 else ~t.isfinite()
+        bad = bad.flatten(2).any(-1)
+        if bool((bad if behind is None else bad & ~behind).any()):
+            return False
+    return not any(bool(t.isnan().any()) for t in params.values()) and (h0 is None or bool(h0.isfinite().all()))
 
 
 def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, scale=None, qk_norm=True, out=None,
@@ -739,9 +752,13 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     a row's end is left as it was (undefined where y is allocated here).
     ``scale`` defaults to N^(-1/2); ``segments`` = 0 lets the library cut the
     sequence for the current device.  ``out`` = (y, h_out); h_out may be h0.
-    With ``check`` the call waits for the device and raises AxonError
-    (AXON_ERR_TIMEOUT) if a wait of the kernel gave up; ``check=False`` returns
-    at once (read the flag with ``delta_error_flag(workspace)``).
+    bf16 sequences but short ones go in chunks on the tensor cores, which need
+    ``workspace`` and may fail; float32 and short ones go token by token.  In
+    chunks the call waits, with ``check``, for the device and raises AxonError:
+    AXON_ERR_TIMEOUT if a wait of a kernel gave up, AXON_ERR_UNSUPPORTED if with
+    ``qk_norm=False`` an operand left fp16's range (keys longer than about 4 can
+    do that).  ``check=False``, and every call token by token, returns at once
+    (read the flag with ``delta_error_flag(workspace)``).
     """
     i, H, P, G, N, io, args = _delta_args("delta_scan", 2, q, k, v, dt_raw, b_raw, params)
     if i != _current_device():
@@ -766,8 +783,12 @@ def delta_scan(q, k, v, dt_raw, b_raw, params: dict, h0=None, *, lengths=None, s
     _check(_lib.axon_delta_scan_fwd(Bsz, L, H, G, P, N, io, *args, _p(lengths), _p(h0),
                                     N ** -0.5 if scale is None else scale, qk_norm, _p(y), _p(h_out), segments,
                                     _p(workspace), wsz, _stream_on(stream, i)), "axon_delta_scan_fwd")
-    if check and nbytes > 0 and delta_error_flag(workspace) != 0:
-        raise AxonError(6, "axon_delta_scan_fwd (a wait for a copy or a tensor-core product gave up)")
+    if check and nbytes > 0:
+        flag = delta_error_flag(workspace)
+        if flag & 1:
+            raise AxonError(6, "axon_delta_scan_fwd (a wait for a copy or a tensor-core product gave up)")
+        if flag and _finite_tokens(lengths, (q, k, v), (dt_raw, b_raw), params, None if h0 is h_out else h0):
+            raise AxonError(2, "axon_delta_scan_fwd (not finite: keys too long for the products' fp16 range)")
     return y, h_out
 
 

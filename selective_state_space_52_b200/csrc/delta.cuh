@@ -41,7 +41,10 @@
 // of the walk is linear in lane v, so S, V, R, U and Y simply live in units of
 // 1 / lambda_v.  Before each chunk a lane whose largest of |S| and |V| has left
 // [2^-3, 2^6] rescales; with keys of length at most 1 no product of the chunk
-// then exceeds 64 (1 + 64) + 64 sqrt(N) < 2^13, far inside fp16.
+// then exceeds 64 (1 + 64) + 64 sqrt(N) < 2^13, far inside fp16.  Raw keys may
+// be longer; an operand that then leaves fp16's range comes out as infinity or
+// NaN in y or in the end state (zeros of T and M times infinity are NaN, and S
+// keeps one), and where either is not finite the error flag says so.
 // Two bf16 parts (no scale needed) came to 4.5e-6 on the final state in a
 // float64 model of these roundings, and three to half again as many products;
 // measured with fp16 parts: 5e-7.  Y's products take both parts of S, U and M
@@ -73,7 +76,7 @@ struct DeltaChunkParams {
     int nC;                      // chunks of L
     unsigned char* kq;           // (B, G, nC): K', then Q': fp16, 64 rows in 64-column blocks, 128-byte swizzle
     unsigned char* blob;         // (B, H, nC): kDlBlob bytes
-    int* err;                    // set to 1 when a wait gave up
+    int* err;                    // bits: 1 a wait gave up, 2 y or the end state is not finite (told with raw keys only)
     // the sequence in segments of cps chunks, when there are few heads:
     int segs, cps;
     float* sloc;                 // (segs - 1, B, H, P, N): a segment's end state from zeros (the first: from h0)
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
     const bool failed = __syncthreads_or(!ok);           // KQ is free from here on: A, M and W lie over it
     const bool drained = !failed || mbar_wait(sb + Lay::MB, 0u);
     tc_fence_after();
-    if (failed && tid == 0) atomicExch(p.err, 1);
+    if (failed && tid == 0) atomicOr(p.err, 1);
 
     const int r = d.H / d.G;
     const int i = tid & 63;                              // this thread's row of A (warps 0, 1) or M (2, 3)
@@ -980,6 +983,12 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                     const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
                     o[q] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
                 }
+                if (!d.norm) {
+                    uint32_t big = 0;                     // bf16 bits order like their values, infinity and NaN last
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) big = __vmaxu2(big, o[q] & 0x7fff7fffu);
+                    if ((big & 0xffffu) >= 0x7f80u || big >> 16 >= 0x7f80u) atomicOr(p.err, 2);
+                }
                 if (len - (cb + c - 1) * C >= C) {        // no token of the chunk is missing
 #pragma unroll
                     for (int q = 0; q < 8; ++q) *reinterpret_cast<uint32_t*>(yo + q * ystep) = o[q];
@@ -1083,6 +1092,13 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
         float* to = kFull ? (cb + max(nC, 0) == all ? d.h_out : nullptr) : trans ? nullptr : p.sloc + seg * hstep;
         if (ok && to) {
             const float ilam = inverse(lam);
+            if (kFull && !d.norm) {
+                uint32_t big = 0;
+#pragma unroll
+                for (int n = 0; n < NQ / 2; ++n)
+                    big = max(big, max(__float_as_uint(S[n].x) & 0x7fffffffu, __float_as_uint(S[n].y) & 0x7fffffffu));
+                if (big >= 0x7f800000u) atomicOr(p.err, 2);
+            }
 #pragma unroll
             for (int n = 0; n < NQ; n += 4)
                 *reinterpret_cast<float4*>(to + hoff + n) =
@@ -1096,7 +1112,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
         bool drained = !*dead;                            // else some wait gave up, in this warp or another
         if (!drained) {
             if (elect_one()) {
-                atomicExch(p.err, 1);
+                atomicOr(p.err, 1);
                 umma_commit(bar(Lay::DRAIN));
             }
             __syncwarp();

@@ -625,3 +625,77 @@ def test_raw_queries_of_any_length(cuda_lib, power, segments):
     p = 2.0 ** (power - power // 2)
     close(y / p, y_ref / p, 2.6e-3, "y", 1.3e-2)
     close(h / 2.0 ** (-power // 2), h_ref / 2.0 ** (-power // 2), 1e-5, "state")
+
+
+# ------------------------------------------------------------ raw keys too long for the chunks
+def long_keys(what, L=200):
+    inp = make(L=L, B=1)
+    for n in ("q", "k"):
+        t = inp[n].float()
+        inp[n] = (t / t.norm(dim=-1, keepdim=True)).bfloat16()
+    k = inp["k"].float()
+    if what == "growing":            # beta |k|^2 = 4 along one key: the state's part grows by 3 a token, 3^20 in all
+        k[:, 70:90] = 2 * k[:, 70:71]
+        inp["b_raw"][:, 70:90] = 90.0
+        inp["dt_bias"][:] = -60.0
+    elif what == "long":             # one key of 2^20, hardly taken up
+        k[:, 100] *= 2.0 ** 20
+        inp["b_raw"][:, 100] = -30.0
+    elif what == "last token":       # one of the padded last chunk
+        k[:, -1] *= 2.0 ** 20
+    inp["k"] = k.bfloat16()
+    return inp
+
+
+@pytest.mark.parametrize("segments", [1, 3])
+@pytest.mark.parametrize("what", ["growing", "long", "last token"])
+def test_keys_too_long_are_reported(cuda_lib, what, segments):
+    from selective_state_space_52_b200 import axon_ssm
+    inp = long_keys(what)
+    d, params = dev(inp)
+    with pytest.raises(axon_ssm.AxonError) as e:
+        axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"], qk_norm=False, segments=segments)
+    assert e.value.status == 2
+    ws = torch.empty(axon_ssm.axon_delta_workspace_bytes(1, 200, 4, 2, 128, 128, axon_ssm.AXON_BF16, segments),
+                     dtype=torch.uint8, device="cuda")
+    axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"], qk_norm=False, segments=segments, workspace=ws, check=False)
+    assert axon_ssm.delta_error_flag(ws) == 2
+    # the same workspace afterwards: the flag is cleared, and normalised keys may be of any length
+    y, h = axon_ssm.delta_scan(*(d[n] for n in SEQ), params, d["h0"], segments=segments, workspace=ws)
+    assert axon_ssm.delta_error_flag(ws) == 0
+    y_ref, h_ref = ref(inp)
+    close(y.float().cpu().numpy(), y_ref, 2.6e-3, "y", 1.3e-2)
+    close(h.cpu().numpy(), h_ref, 1e-5, "state")
+
+
+@pytest.mark.parametrize("segments", [1, 3])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_nan_with_raw_keys_is_no_error(cuda_lib, segments, ragged):
+    """A NaN or infinity among the inputs comes out as one and is not reported as keys too
+    long; one behind a row's end is no excuse for keys that are."""
+    from selective_state_space_52_b200 import axon_ssm
+    inp = long_keys("none")
+    inp["v"][0, 70, 1, 5] = float("nan")
+    inp["v"][0, 70, 1, 6] = float("inf")
+    inp["dt_raw"][0, 90, 2] = float("nan")
+    kw = dict(lengths=[190]) if ragged else {}
+    n = 190 if ragged else 200
+    y, h = run(inp, qk_norm=False, segments=segments, **kw)
+    for col in (5, 6):
+        assert not np.isfinite(y[0, 128:n, 1, col]).any() and not np.isfinite(h[0, 1, col]).any()
+    assert np.isnan(y[0, 128:n, 2]).all() and np.isnan(h[0, 2]).all()
+    assert np.isfinite(y[0, :, [0, 3]]).all() and np.isfinite(h[0, [0, 3]]).all()
+    if ragged:
+        inp = long_keys("long")
+        inp["v"][0, 195] = float("nan")
+        with pytest.raises(axon_ssm.AxonError):
+            run(inp, qk_norm=False, segments=segments, **kw)
+
+
+def test_keys_too_long_token_by_token(cuda_lib):
+    """The float32 kernel has no such limit."""
+    inp = {n: t.float() if n in SEQ else t for n, t in long_keys("long").items()}
+    y, h = run(inp, qk_norm=False)
+    y_ref, h_ref = ref(inp, qk_norm=False)
+    close(y, y_ref, 1e-5, "y")
+    close(h, h_ref, 1e-5, "state")
