@@ -469,8 +469,9 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * left fp16's range, or an input was not finite.  Read it after the call
  * completes.  Every call writes what it reads in the
  * workspace, so calls that may run at the same time (streams, captured graphs)
- * need one each.  Pointers 16-byte aligned and ldq, ldk, ldv
- * multiples of 8 (bf16) or 4 (f32), else AXON_ERR_ALIGNMENT; y, h_out and the
+ * need one each.  Pointers 16-byte aligned (dt_raw, b_raw, dt_bias, A_log and
+ * lengths: by their own element) and ldq, ldk, ldv multiples of 8 (bf16) or 4
+ * (f32), else AXON_ERR_ALIGNMENT; y, h_out and the
  * workspace overlap no input (but h_out may be h0) nor each other
  * (AXON_ERR_INVALID_ARG).  B, H <= 65535 and B*L*H <= 2^31, else
  * AXON_ERR_UNSUPPORTED.  B == 0 or H == 0 is a no-op; L == 0 copies h0 (or

@@ -64,8 +64,12 @@ axon_status check_delta(size_t rows, int H, int G, int P, int N, axon_dtype io, 
     if (ldq < G * N || ldk < G * N || ldv < H * P) return AXON_ERR_INVALID_ARG;
     const int m = io == AXON_BF16 ? 8 : 4;
     if (ldq % m || ldk % m || ldv % m) return AXON_ERR_ALIGNMENT;
-    for (const void* t : {q, k, v, dt_raw, b_raw, (const void*)dt_bias, (const void*)A_log})
+    for (const void* t : {q, k, v})
         if (t && !al16(t)) return AXON_ERR_ALIGNMENT;
+    // the rates and parameters are read one value at a time
+    const uintptr_t gate = reinterpret_cast<uintptr_t>(dt_raw) | reinterpret_cast<uintptr_t>(b_raw);
+    const uintptr_t par = reinterpret_cast<uintptr_t>(dt_bias) | reinterpret_cast<uintptr_t>(A_log);
+    if ((gate & (io == AXON_BF16 ? 1u : 3u)) || (par & 3u)) return AXON_ERR_ALIGNMENT;
     return AXON_OK;
 }
 

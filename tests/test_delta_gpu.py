@@ -699,3 +699,25 @@ def test_keys_too_long_token_by_token(cuda_lib):
     y_ref, h_ref = ref(inp, qk_norm=False)
     close(y, y_ref, 1e-5, "y")
     close(h, h_ref, 1e-5, "state")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [1, 3, 4])
+def test_rates_at_any_token(cuda_lib, io, H):
+    """One sequence's rates of any token, and parameters out of a longer array: contiguous, aligned only to a value."""
+    from selective_state_space_52_b200 import axon_ssm
+    L = 70
+    inp = make(G=1, H=H, io=io, L=L, B=1)
+    d, params = dev(inp)
+    params = {n: torch.cat([t.new_zeros(1), t])[1:] for n, t in params.items()}
+    state = d["h0"].clone()
+    y_ref, h_ref = ref(inp)
+    ys = [axon_ssm.delta_step(*(d[n][:, t] for n in SEQ), params, state) for t in range(3)]
+    y, h = axon_ssm.delta_scan(*(d[n][:, 3:] for n in SEQ), params, state)
+    ys = torch.cat([*(t[:, None] for t in ys), y], 1).float().cpu().numpy()
+    close(ys, y_ref, tols(io)[0], "y", tols(io)[1])
+    close(h.cpu().numpy(), h_ref, 1e-5, "state")
+    if io == "bf16":
+        y, h = axon_ssm.delta_scan(*(d[n][:, 3:] for n in SEQ), params, state, segments=1)
+        close(y.float().cpu().numpy(), y_ref[:, 3:], 2.6e-3, "y in chunks", 1.3e-2)
+        close(h.cpu().numpy(), h_ref, 1e-5, "state in chunks")

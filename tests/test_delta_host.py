@@ -329,3 +329,19 @@ def test_the_largest_stride_passes(lib):
     last = (1 << 31) - 8
     assert _row_stride("f", "t", far_apart(last, 128), 2, 128) == last
     assert _token_stride("f", "t", far_apart(last, 2, 64)) == last
+
+
+# ------------------------------------------------------------ alignment: what the kernels' loads need, no more
+GATES = dict(dt_raw=3, b_raw=4)
+PARAMS = dict(dt_bias=5, A_log=6)
+
+
+@pytest.mark.parametrize("call", [scan, step])
+@pytest.mark.parametrize("io", [0, 1])
+@pytest.mark.parametrize("name", [*GATES, *PARAMS])
+def test_delta_rates_need_their_own_alignment(lib, call, io, name):
+    """A value's own alignment passes (the call then fails for y over q), less does not."""
+    at = FAKE + ({**GATES, **PARAMS}[name] << 24)
+    size = 2 if io == 1 and name in GATES else 4
+    assert call(lib, io=io, **{name: at + size}, y=FAKE) == 1
+    assert call(lib, io=io, **{name: at + size // 2}, y=FAKE) == 3
