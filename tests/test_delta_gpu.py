@@ -721,3 +721,43 @@ def test_rates_at_any_token(cuda_lib, io, H):
         y, h = axon_ssm.delta_scan(*(d[n][:, 3:] for n in SEQ), params, state, segments=1)
         close(y.float().cpu().numpy(), y_ref[:, 3:], 2.6e-3, "y in chunks", 1.3e-2)
         close(h.cpu().numpy(), h_ref, 1e-5, "state in chunks")
+
+
+# ------------------------------------------------------------ long sequences, cut as long prompts are
+@pytest.mark.parametrize("N, P", [(64, 64), (64, 128), (128, 64), (128, 128)])
+def test_long_segments_after_a_fold(cuda_lib, N, P):
+    """21 chunks in three segments of seven: the last enters with a fold and then goes
+    more than twice round the three stages that held the transitions."""
+    check(make(N, P, 1, 2, L=1300, B=1), f"three segments, N{N} P{P}", segments=3)
+
+
+@pytest.mark.parametrize("segments", [3, 4])
+def test_long_segments_of_ragged_rows(cuda_lib, segments):
+    """Rows that end in every segment and at a segment's and a chunk's end, in place and without a state."""
+    lengths = [1300, 1299, 1090, 897, 896, 500, 448, 64, 0]
+    inp = make(G=1, H=2, B=len(lengths), L=1300)
+    check(inp, f"{segments} segments in place", segments=segments, lengths=lengths, in_place=True)
+    check(inp, f"{segments} segments, no h0", segments=segments, lengths=lengths, h0=False)
+
+
+@pytest.mark.parametrize("segments", [0, 1, 3, 8])
+def test_long_memory(cuda_lib, segments):
+    """4096 tokens whose decays keep some thousand of them; segments = 0 cuts the sequence.
+    A chunk's error is 2^-22 an operand and five products, of either sign over the
+    64 chunks: sqrt(64 * 5) 2^-22 = 4.3e-6, asserted as everywhere at 1e-5."""
+    from selective_state_space_52_b200 import axon_ssm
+    inp = make(G=1, H=2, L=4096, B=1)
+    inp["dt_bias"][:] = torch.tensor([-7.0, -8.0])
+    inp["A_log"][:] = 0.0
+    if segments == 0:
+        size = lambda s: axon_ssm.axon_delta_workspace_bytes(1, 4096, 2, 1, 128, 128, axon_ssm.AXON_BF16, s)    # noqa: E731
+        assert size(0) > size(1)
+    check(inp, "long memory", segments=segments)
+
+
+def test_cut_by_the_library(cuda_lib):
+    """One chunk short of a full cut, few heads: the library's own segments."""
+    from selective_state_space_52_b200 import axon_ssm
+    size = lambda s: axon_ssm.axon_delta_workspace_bytes(2, 2047, 2, 1, 128, 64, axon_ssm.AXON_BF16, s)      # noqa: E731
+    assert size(0) > size(1)
+    check(make(128, 64, 1, 2, L=2047, B=2), "the library's segments", lengths=[2047, 1111])
