@@ -97,18 +97,21 @@ void launch_recur(const DeltaParams& p, cudaStream_t st) {
 
 constexpr int kDlMaxSegs = 64;
 // Whether bf16 sequences go in chunks: on request (segments > 0), or when that
-// is faster.  Measured, in us, with x = B H P N / 128^2: a token of the
-// token-by-token kernel takes 0.15 + 0.0035 x; one chunk costs 23 (N = 128) or
-// 14 (N = 64), most of it the start of two launches, or a SM's share of that
-// with many heads, and each further one 3.  (B1 H8: 64 tokens 15 against 24,
-// 128 tokens 27 against 26; B8 H16: 32 tokens 22 against 24, 48 tokens 31
-// against 24; B32 H32: 24 tokens 100 against 115, 32 tokens 127 against 116.)
+// is faster.  Measured on the device, in us, with x = B H N P / 128^2: a call
+// token by token takes 1 and then max(0.2, 0.13 + 0.0035 x) a token; one chunk
+// 22 (N = 128) or 18 (N = 64), most of it the start of two launches, or a SM's
+// share of that with many heads, and each further one 3.  Token by token
+// against chunks, N = P = 128: B1 H8, 96 tokens 22 and 28, 128 tokens 28 and
+// 28, 160 tokens 34 and 31; B8 H16, 32 tokens 23 and 26, 48 tokens 32 and 26;
+// B32 H32, 24 tokens 101 and 124, 32 tokens 128 and 125.  N = P = 64: B1 H8,
+// 80 tokens 17 and 21, 128 tokens 26 and 21; B32 H32, 48 tokens 55 and 71, 96
+// tokens 104 and 117, 128 tokens 139 and 115.
 bool chunked(int B, int L, int H, int P, int N, axon_dtype io, int segments) {
     if (io != AXON_BF16 || L <= 0) return false;
     if (segments > 0) return true;
     const double bh = (double)B * H, x = bh * P * N / 16384.0;
-    const double chunks = (N == 128 ? 23.0 : 14.0) * std::max(1.0, bh / 205.0) + 3.0 * ((L - 1) / kDlC);
-    return chunks < L * (0.15 + 0.0035 * x);
+    const double first = N == 128 ? std::max(22.0, 0.115 * bh) : std::max(18.0, 0.08 * bh);
+    return first + 3.0 * ((L - 1) / kDlC) < 1.0 + L * std::max(0.2, 0.13 + 0.0035 * x);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }

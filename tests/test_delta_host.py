@@ -345,3 +345,14 @@ def test_delta_rates_need_their_own_alignment(lib, call, io, name):
     size = 2 if io == 1 and name in GATES else 4
     assert call(lib, io=io, **{name: at + size}, y=FAKE) == 1
     assert call(lib, io=io, **{name: at + size // 2}, y=FAKE) == 3
+
+
+@pytest.mark.parametrize("B, L, H, P, N, chunks", [
+    # measured on the device, us token by token and in chunks: wherever one takes a fifth more, the other is chosen
+    (1, 96, 8, 128, 128, False), (1, 160, 1, 128, 128, True), (1, 160, 8, 64, 128, True), (1, 112, 1, 64, 64, True),
+    (1, 80, 8, 64, 64, False), (1, 128, 8, 64, 64, True), (8, 32, 32, 128, 64, False), (8, 48, 32, 64, 64, False),
+    (8, 48, 16, 128, 128, True), (32, 24, 32, 128, 128, False), (32, 48, 32, 128, 128, True), (32, 48, 32, 64, 64, False),
+    (32, 128, 32, 64, 64, True),
+])
+def test_delta_path_is_the_faster_one(lib, B, L, H, P, N, chunks):
+    assert (lib.axon_delta_workspace_bytes(B, L, H, 1, P, N, 1, 0) > 0) == chunks
