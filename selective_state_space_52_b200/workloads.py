@@ -283,8 +283,6 @@ class DeltaWorkload:
 
 
 DELTA_WORKLOADS = [
-    DeltaWorkload("delta_layer", 1, 4096, 16, 32, 31,
-                  note="32 value heads of 128 on 16 key heads of 128, bf16"),
     DeltaWorkload("small_delta", 2, 130, 2, 4, 32, note="small case for parity tests"),
 ]
 DELTA_WORKLOAD_BY_NAME = {w.name: w for w in DELTA_WORKLOADS}
