@@ -491,6 +491,17 @@ AXON_API axon_status axon_delta_scan_fwd(
     const int *lengths, const float *h0, float scale, int qk_norm,
     void *y, float *h_out, int segments, void *workspace, size_t workspace_bytes, axon_stream_t stream);
 
+/*
+ * The failure path of the chunked walk in isolation (tests): one block whose
+ * first warp waits, for `limit` polls (1 .. 65536), on an mbarrier that nothing
+ * arrives on, while its second waits on another until the first has given up;
+ * then the block drains its (absent) products and frees its tensor memory.
+ * status (two device ints, 4-byte aligned): [0] bit 0 the first warp gave up,
+ * bit 1 the second did, bit 2 the drain completed; [1] the error flag.
+ * AXON_ERR_INVALID_ARG for a NULL or misaligned status or another limit.
+ */
+AXON_API axon_status axon_delta_wait_probe(int *status, int limit, axon_stream_t stream);
+
 AXON_API axon_status axon_delta_step(
     int B, int H, int G, int P, int N, axon_dtype io,
     const void *q, int ldq, const void *k, int ldk, const void *v, int ldv,

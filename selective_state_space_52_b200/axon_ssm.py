@@ -81,6 +81,8 @@ _lib.axon_delta_workspace_bytes.argtypes = [_i] * 8
 _lib.axon_delta_scan_fwd.restype = _i
 _lib.axon_delta_scan_fwd.argtypes = ([_i] * 7 + [_vp, _i] * 3 + [_vp] * 6 + [ctypes.c_float, _i] +
                                      [_vp] * 2 + [_i, _vp, _sz, _vp])
+_lib.axon_delta_wait_probe.restype = _i
+_lib.axon_delta_wait_probe.argtypes = [_vp, _i, _vp]
 _lib.axon_delta_step.restype = _i
 _lib.axon_delta_step.argtypes = [_i] * 6 + [_vp, _i] * 3 + [_vp] * 4 + [ctypes.c_float, _i] + [_vp] * 3
 _lib.axon_gated_norm_fwd.restype = _i
@@ -306,6 +308,13 @@ def axon_ssd_scan_fwd(B, L, H, P, N, io, x, dt_raw, dt_bias, A_log, Bm, Cm, D, h
 
 def axon_delta_workspace_bytes(B, L, H, G, P=128, N=128, io=AXON_BF16, segments=0) -> int:
     return int(_lib.axon_delta_workspace_bytes(B, L, H, G, P, N, io, segments))
+
+
+def axon_delta_wait_probe(status, limit, stream=None, *, raise_on_error=True) -> int:
+    rc = _lib.axon_delta_wait_probe(_p(status), int(limit), _stream(stream))
+    if raise_on_error:
+        _check(rc, "axon_delta_wait_probe")
+    return rc
 
 
 def axon_ssm_block_workspace_bytes(B, L, Dm, E, N=16, K=4, io=AXON_BF16) -> int:

@@ -304,6 +304,12 @@ axon_status axon_delta_scan_fwd(int B, int L, int H, int G, int P, int N, axon_d
     return cudaGetLastError() == cudaSuccess ? AXON_OK : AXON_ERR_CUDA;
 }
 
+axon_status axon_delta_wait_probe(int* status, int limit, axon_stream_t stream) {
+    if (!status || (reinterpret_cast<uintptr_t>(status) & 3u) || limit < 1 || limit > (1 << 16)) return AXON_ERR_INVALID_ARG;
+    delta_wait_probe_kernel<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(status, limit);
+    return cudaGetLastError() == cudaSuccess ? AXON_OK : AXON_ERR_CUDA;
+}
+
 axon_status axon_delta_step(int B, int H, int G, int P, int N, axon_dtype io,
                             const void* q, int ldq, const void* k, int ldk, const void* v, int ldv,
                             const void* dt_raw, const void* b_raw, const float* dt_bias, const float* A_log,

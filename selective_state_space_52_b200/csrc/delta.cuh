@@ -548,16 +548,57 @@ struct DeltaWalkSmem {
 
 // The warp waits for an mbarrier's phase; gives up after a bounded number of
 // polls, or when another warp of the block has.  The same answer in every lane.
-__device__ __forceinline__ bool delta_wait(uint32_t mbar, int use, volatile int* dead) {
+__device__ __forceinline__ bool delta_wait(uint32_t mbar, int use, volatile int* dead, int limit = kTcWaitLimit) {
     if (__all_sync(0xffffffffu, mbar_wait(mbar, (uint32_t)(use & 1), 1))) return true;
     bool ok = false;
-    for (int k = 0; k < 4096 && !ok; ++k) {
-        ok = mbar_wait(mbar, (uint32_t)(use & 1), kTcWaitLimit / 4096);
+    for (int k = 0; k < limit && !ok; k += 1024) {
+        ok = mbar_wait(mbar, (uint32_t)(use & 1), min(limit - k, 1024));
         if (!ok && *dead) break;
     }
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) *dead = 1;
     return ok;
+}
+// After a wait gave up: tells the host, and whether the products that this
+// warp's elected lane has issued are all done (a bounded wait); only then may
+// their tensor memory go to another block.
+__device__ __forceinline__ bool delta_drain(uint32_t mbar, int* err) {
+    if (elect_one()) {
+        atomicOr(err, 1);
+        umma_commit(mbar);
+    }
+    __syncwarp();
+    return __all_sync(0xffffffffu, mbar_wait(mbar, 0u));
+}
+// The walk's failure path by itself: warp 0 waits `limit` polls for an mbarrier
+// that nothing arrives on, warp 1 (with the walk's own limit) for another until
+// warp 0 has given up; then the drain, with no product in flight, and the
+// tensor memory is freed.  status[0]: bit 0 warp 0 gave up, 1 warp 1 did, 2
+// drained; status[1]: the error flag.  grid = 1, 64 threads.
+__global__ void __launch_bounds__(64) delta_wait_probe_kernel(int* status, int limit) {
+    __shared__ __align__(8) unsigned long long bars[3];
+    __shared__ int dead, slot, got;
+    const uint32_t mb = static_cast<uint32_t>(__cvta_generic_to_shared(bars));
+    const int w = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 3; ++i) mbar_init(mb + 8 * i, 1);
+        dead = 0;
+        got = 0;
+        status[1] = 0;
+        fence_mbar_init();
+    }
+    if (w == 0) tmem_alloc(static_cast<uint32_t>(__cvta_generic_to_shared(&slot)), 32);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const bool done = delta_wait(mb + 8 * w, 0, &dead, w == 0 ? limit : kTcWaitLimit);
+    if (!done && (threadIdx.x & 31) == 0) atomicOr(&got, 1 << w);
+    __syncthreads();
+    if (w == 0) {
+        const bool drained = delta_drain(mb + 16, status + 1);
+        if (drained) tmem_dealloc(*reinterpret_cast<volatile int*>(&slot), 32);
+        if (threadIdx.x == 0) status[0] = got | (drained ? 4 : 0);
+    }
 }
 // 8 consecutive columns of this thread's tensor-memory lane; 4 into it
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
@@ -1110,14 +1151,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
     tc_fence_after();
     if (w == 16) {
         bool drained = !*dead;                            // else some wait gave up, in this warp or another
-        if (!drained) {
-            if (elect_one()) {
-                atomicOr(p.err, 1);
-                umma_commit(bar(Lay::DRAIN));
-            }
-            __syncwarp();
-            drained = __all_sync(0xffffffffu, mbar_wait(bar(Lay::DRAIN), 0u));
-        }
+        if (!drained) drained = delta_drain(bar(Lay::DRAIN), p.err);
         if (drained) tmem_dealloc(tbase, Lay::COLS);      // a late product must not meet another block's columns
     }
 }

@@ -761,3 +761,16 @@ def test_cut_by_the_library(cuda_lib):
     size = lambda s: axon_ssm.axon_delta_workspace_bytes(2, 2047, 2, 1, 128, 64, axon_ssm.AXON_BF16, s)      # noqa: E731
     assert size(0) > size(1)
     check(make(128, 64, 1, 2, L=2047, B=2), "the library's segments", lengths=[2047, 1111])
+
+
+def test_wait_gives_up_and_reports(cuda_lib):
+    """The walk's failure path: a wait that nothing ends gives up, the block's other waits
+    end with it, the flag is set, products are drained and the tensor memory is freed, so
+    that the chunked kernels (which need all of an SM's) run as before afterwards."""
+    from selective_state_space_52_b200 import axon_ssm
+    for limit in (1, 64, 3000):
+        status = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+        axon_ssm.axon_delta_wait_probe(status, limit)
+        torch.cuda.synchronize()
+        assert status.tolist() == [7, 1], limit
+    check(make(G=16, H=32, B=5, L=100), "after the probe", segments=1)

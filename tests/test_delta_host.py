@@ -356,3 +356,9 @@ def test_delta_rates_need_their_own_alignment(lib, call, io, name):
 ])
 def test_delta_path_is_the_faster_one(lib, B, L, H, P, N, chunks):
     assert (lib.axon_delta_workspace_bytes(B, L, H, 1, P, N, 1, 0) > 0) == chunks
+
+
+def test_delta_wait_probe_rejects_bad_arguments(lib):
+    f = lib.axon_delta_wait_probe
+    for status, limit, want in ((None, 64, 1), (FAKE, 0, 1), (FAKE, -5, 1), (FAKE, (1 << 16) + 1, 1), (FAKE + 2, 64, 1)):
+        assert f(status, limit, None) == want
