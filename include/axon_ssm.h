@@ -431,10 +431,12 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * whose products take fp16 parts, is made for keys of length near 1: with
  * longer ones than about 4 an operand can leave fp16's range, which shows as
  * infinity or NaN and in the error flag; with all keys at length l < 1 the state's relative error
- * is some 1e-6 / l.  Queries may have any length.  In chunks a value column
- * of 64 tokens and the state before them keep 21 bits of their largest value:
- * what is smaller by more than that, in the same chunk, is lost.  Token by
- * token neither limit holds.)
+ * is some 1e-6 / l.  Queries may have any length.  In chunks the state before
+ * 64 tokens and what they write, a value column at a time, keep 21 bits of
+ * the larger of the two: writes smaller by more than that than a state which
+ * the same chunk forgets are lost.  Token by token neither limit holds.
+ * |k|^2 and |q|^2 are float32: with the norm, rows longer than 1.8e19 count
+ * as zeros.)
  *
  * axon_delta_scan_fwd, prefill.  Layouts: q, k (B,L,G,N) and v (B,L,H,P) io,
  * consecutive tokens ldq, ldk, ldv elements apart (ldq, ldk >= G*N, ldv >=

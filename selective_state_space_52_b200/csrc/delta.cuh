@@ -16,6 +16,10 @@
 // one before it, so the walk is bound by that chain (about half of it tensor
 // products, half the conversions between them), not by bandwidth.
 //
+// fp16 has no room for small beta (sigmoid(-10) is below its smallest normal
+// number), so with theta the power of two above a chunk's largest beta T is
+// kept over theta and R times theta; their product is U all the same.
+//
 // Everything in the walk is kept transposed, so that a tensor-memory lane is
 // one value column v (M = 128 lanes): S^T row v, R^T, U^T and Y^T rows are all
 // in lane v and belong to one thread, which holds the float32 state row in
@@ -39,7 +43,7 @@
 // fp16 parts, hi + lo, 21 significant bits; the lo x lo term is dropped.  fp16
 // needs values near 1, so each lane carries a power-of-two scale lambda_v: all
 // of the walk is linear in lane v, so S, V, R, U and Y simply live in units of
-// 1 / lambda_v.  Before each chunk a lane whose largest of |S| and |V| has left
+// 1 / lambda_v.  Before each chunk a lane whose largest of |S| and theta |V| has left
 // [2^-3, 2^6] rescales; with keys of length at most 1 no product of the chunk
 // then exceeds 64 (1 + 64) + 64 sqrt(N) < 2^13, far inside fp16.  Raw keys may
 // be longer; an operand that then leaves fp16's range comes out as infinity or
@@ -63,7 +67,7 @@ namespace axon {
 
 constexpr int kDlC = 64;                       // tokens per chunk
 constexpr int kDlTile = kDlC * kDlC * 2;       // a 64 x 64 fp16 tile: 8 KB
-constexpr int kDlVec = 4 * kDlC * 4;           // four rows, a value a token: -e^Gamma rk, e^Gamma, e^(Gamma_last - Gamma) rk, scale rq
+constexpr int kDlVec = 4 * kDlC * 4;           // four rows, a value a token: -theta e^Gamma rk, e^Gamma, e^(Gamma_last - Gamma) rk, scale rq
 // Per chunk and value head: T hi, T lo, M hi, vectors.  The three matrices are
 // lower triangular, and no product reads their upper right 32 x 32 blocks:
 // those hold the three other blocks of M lo (T hi's: rows and columns 0 .. 31,
@@ -103,6 +107,17 @@ __device__ __forceinline__ void split_f16(float2 x, uint32_t& hi, uint32_t& lo) 
     hi = pack_f16(h0, h1);
     lo = pack_f16(x.x - h0, x.y - h1);
 }
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }    // -126 <= e <= 127
+
+// For m > 0 the exponent e with m 2^-e in [1/2, 1); ..
+__device__ __forceinline__ int exp_of(float m) { return (int)((__float_as_uint(m) >> 23) & 255u) - 126; }
+// .. held to what a float power of two and its inverse can say (m 2^-e < 4).
+__device__ __forceinline__ int exp_above(float m) { return min(max(exp_of(m), -126), 126); }
+// theta's exponent from the largest b_raw of a chunk (-inf: no token): prep and walk agree to the bit
+__device__ __forceinline__ int theta_exp(float b_max) {
+    const float beta = delta_beta(b_max);
+    return beta > 0.f ? exp_of(beta) : 0;
+}
 // a b + c with a and b in bf16
 __device__ __forceinline__ float fma_bf16(unsigned short a, unsigned short b, float c) {
     float d;
@@ -120,13 +135,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                  ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }    // -126 <= e <= 127
-
-// For m > 0 the exponent e with m 2^-e in [1/2, 1); ..
-__device__ __forceinline__ int exp_of(float m) { return (int)((__float_as_uint(m) >> 23) & 255u) - 126; }
-// .. held to what a float power of two and its inverse can say (m 2^-e < 4).
-__device__ __forceinline__ int exp_above(float m) { return min(max(exp_of(m), -126), 126); }
-
 // ---- prep: grid = (nC, G, B), 128 threads.  What bounds it is latency and the
 // instruction caches (six blocks an SM in different phases), so the loops are
 // kept short: forward substitution down whole columns, unrolled over
@@ -149,9 +157,11 @@ struct DeltaPrepSmem {
     static constexpr int GH = RQ + kDlC * 4;             // two heads: Gamma (log2 units), float hi and lo parts
     static constexpr int GL = GH + 2 * kDlC * 4;
     static constexpr int BE = GL + 2 * kDlC * 4;         // beta
-    static constexpr int VJ = BE + 2 * kDlC * 4;         // e^(Gamma_r - Gamma_j) rk'_j, r the last of j's 16 tokens
+    static constexpr int BT = BE + 2 * kDlC * 4;         // beta / theta
+    static constexpr int VJ = BT + 2 * kDlC * 4;         // e^(Gamma_r - Gamma_j) rk'_j, r the last of j's 16 tokens
     static constexpr int TOT = VJ + 2 * kDlC * 4;        // doubles: the first warps' totals
-    static constexpr int MB = TOT + 16;
+    static constexpr int BM = TOT + 16;                  // the warps' largest b_raw
+    static constexpr int MB = BM + 16;
     static constexpr int SLOT = MB + 8;
     static constexpr int BYTES = SLOT + 8;
     static constexpr int TOTAL = BYTES + 1024;           // with the alignment pad
@@ -366,6 +376,7 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
         const float* gh = reinterpret_cast<const float*>(sm + Lay::GH) + slot * C;
         const float* gl = reinterpret_cast<const float*>(sm + Lay::GL) + slot * C;
         const float* be = reinterpret_cast<const float*>(sm + Lay::BE) + slot * C;
+        const float* bt = reinterpret_cast<const float*>(sm + Lay::BT) + slot * C;
         const float* vj = reinterpret_cast<const float*>(sm + Lay::VJ) + slot * C;
         if (slot == 0) {
             // ---- the rates of two heads (warps 0, 1 and 2, 3), a token a lane.  The
@@ -373,15 +384,20 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
             // differences of neighbours count.
             const int mine = tid >> 6, hm = h + mine;
             const bool have = hh + mine < r;
-            float lg = 0.f, beta = 0.f;
+            float lg = 0.f, beta = 0.f, bm = -INFINITY;
             if (live && have) {
                 const size_t o = ((size_t)b * d.L + t0 + i) * d.H + hm;
                 lg = delta_log2_decay(IoBF16::load(static_cast<const __nv_bfloat16*>(d.dt_raw) + o) + __ldg(d.dt_bias + hm),
                                       delta_exp_a(__ldg(d.A_log + hm)));
                 // a decay below 2^-2000 is 0 to a float anyway, and an infinite one would leave inf - inf
                 lg = lg < -2000.f ? -2000.f : lg;
-                beta = delta_beta(IoBF16::load(static_cast<const __nv_bfloat16*>(d.b_raw) + o));
+                bm = IoBF16::load(static_cast<const __nv_bfloat16*>(d.b_raw) + o);
+                beta = delta_beta(bm);
             }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+            float* bms = reinterpret_cast<float*>(sm + Lay::BM);
+            if (lane == 0) bms[w] = bm;
             double G = (double)lg;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -395,6 +411,8 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
             reinterpret_cast<float*>(sm + Lay::BE)[mine * C + i] = beta;
             __syncthreads();
             if (w & 1) G += *tot;
+            const int te = theta_exp(fmaxf(bms[2 * mine], bms[2 * mine + 1]));
+            reinterpret_cast<float*>(sm + Lay::BT)[mine * C + i] = beta * pow2i(-te);
             const float hi = (float)G, lo = (float)(G - (double)hi);
             gh2[i] = hi;
             gl2[i] = lo;
@@ -403,7 +421,7 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
             const float eg = ex2_approx(hi);
             float* v2 = reinterpret_cast<float*>(sm + Lay::V) + mine * 4 * C;
             reinterpret_cast<float*>(sm + Lay::VJ)[mine * C + i] = ex2_approx((gh2[r16] - hi) + (gl2[r16] - lo)) * rk[i];
-            v2[i] = -eg * rk[i];
+            v2[i] = -(eg * rk[i]) * pow2i(te);
             v2[C + i] = eg;
             v2[2 * C + i] = ex2_approx((gh2[C - 1] - hi) + (gl2[C - 1] - lo)) * rk[i];
             v2[3 * C + i] = rq[i];
@@ -465,7 +483,7 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
             }
         }
         __syncthreads();
-        // ---- the blob: T = (I + A)^-1 diag(beta) as fp16 hi and lo tiles, M, the vectors
+        // ---- the blob: T = (I + A)^-1 diag(beta / theta) as fp16 hi and lo tiles, M, the vectors
         unsigned char* blob = p.blob + (((size_t)b * d.H + h) * p.nC + c) * kDlBlob;
         if (w >= 2) {                                    // beside the diagonal blocks' inversion by warps 0 and 1
 #pragma unroll
@@ -479,7 +497,7 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
             const int row = (tid >> 3) + 16 * k, pc = tid & 7;
             const float4 a0 = *reinterpret_cast<const float4*>(A + row * Lay::LDA + 8 * pc);
             const float4 a1 = *reinterpret_cast<const float4*>(A + row * Lay::LDA + 8 * pc + 4);
-            const float4 b0 = *reinterpret_cast<const float4*>(be + 8 * pc), b1 = *reinterpret_cast<const float4*>(be + 8 * pc + 4);
+            const float4 b0 = *reinterpret_cast<const float4*>(bt + 8 * pc), b1 = *reinterpret_cast<const float4*>(bt + 8 * pc + 4);
             uint4 hi, lo;
             split_f16(make_float2(a0.x * b0.x, a0.y * b0.y), hi.x, lo.x);
             split_f16(make_float2(a0.z * b0.z, a0.w * b0.w), hi.y, lo.y);
@@ -526,8 +544,9 @@ struct DeltaWalkSmem {
     static constexpr int VEC = M + kDlTile;
     static constexpr int V = VEC + kDlVec;                // 64 rows of P bf16
     static constexpr int STAGE = V + V_BYTES;
-    static constexpr int VM = kDlStages * STAGE;          // largest |v| of the columns, per stage
-    static constexpr int SMAX = VM + kDlStages * P * 4;   // largest |S| of the quarters of a lane's state row
+    static constexpr int VM = kDlStages * STAGE;          // theta times the largest |v| of the columns, per stage; theta
+    static constexpr int VMS = P * 4 + 16;
+    static constexpr int SMAX = VM + kDlStages * VMS;     // largest |S| of the quarters of a lane's state row
     static constexpr int MB = SMAX + 4 * 128 * 4;
     enum { FULL, VMAX = FULL + kDlStages, X_K0 = VMAX + kDlStages, X_K1, X_Q, U_0, U_1, Y_M, D, D_HI, S_IN, R_IN0, R_IN1, U_IN0,
            U_IN1, Y_OUT, QUAD, DRAIN = QUAD + 4, TR_FULL, BARS = TR_FULL + 2 };
@@ -821,12 +840,17 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
         }
         __syncwarp();
     } else if (w == 17) {
-        // ---------------- the largest |v| of each column (bf16 bits order like their values)
+        // ---------------- the largest |v| of each column (bf16 bits order like their values), and theta
         constexpr int PW = P / 64;                        // words (column pairs) a lane
         for (int c = 0, st = 0, use = 0; c < nC && !trans; ++c) {
+            const int rows = min(C, len - (cb + c) * C);
+            const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(d.b_raw) + ((size_t)b * d.L + (cb + c) * C + lane) * d.H + h;
+            float bm = fmaxf(lane < rows ? IoBF16::load(bp) : -INFINITY, lane + 32 < rows ? IoBF16::load(bp + (size_t)32 * d.H) : -INFINITY);
             if (!delta_wait(bar(Lay::FULL + st), use, dead)) break;
             const uint32_t* v = reinterpret_cast<const uint32_t*>(sm + st * Lay::STAGE + Lay::V) + lane * PW;
-            const int rows = min(C, len - (cb + c) * C);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+            const float theta = pow2i(theta_exp(bm));
             uint32_t m[PW];
 #pragma unroll
             for (int i = 0; i < PW; ++i) m[i] = 0;
@@ -834,9 +858,11 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             for (int t = 0; t < rows; ++t)
 #pragma unroll
                 for (int i = 0; i < PW; ++i) m[i] = __vmaxu2(m[i], v[t * (P / 2) + i] & 0x7fff7fffu);
-            float* vm = reinterpret_cast<float*>(sm + Lay::VM) + st * P + 2 * PW * lane;
+            float* vm = reinterpret_cast<float*>(sm + Lay::VM + st * Lay::VMS);
 #pragma unroll
-            for (int i = 0; i < PW; ++i) *reinterpret_cast<float2*>(vm + 2 * i) = make_float2(bf16_lo(m[i]), bf16_hi(m[i]));
+            for (int i = 0; i < PW; ++i)
+                *reinterpret_cast<float2*>(vm + 2 * PW * lane + 2 * i) = make_float2(theta * bf16_lo(m[i]), theta * bf16_hi(m[i]));
+            if (lane == 0) vm[P] = theta;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(Lay::VMAX + st));
             if (++st == ST) { st = 0; ++use; }
@@ -948,7 +974,7 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
                         if (c < nC && !(ok = delta_wait(bar(Lay::FULL + st), use, dead))) break;
                     } else {
                         if (!(ok = delta_wait(bar(Lay::VMAX + st), use, dead))) break;
-                        vm = reinterpret_cast<const float*>(sm + Lay::VM)[st * P + v];
+                        vm = reinterpret_cast<const float*>(sm + Lay::VM + st * Lay::VMS)[v];
                     }
                     const float both = fmaxf(m, lam * vm);    // infinite or 0 where the product leaves float's range
                     const bool out = both > 64.f || (both < 0.125f && (m > 0.f || vm > 0.f));
@@ -1042,10 +1068,11 @@ __global__ void __launch_bounds__(kDlThreads, 1) delta_walk_kernel(const __grid_
             if (c == nC) break;
             const float* vec = reinterpret_cast<const float*>(sg + Lay::VEC);
             const unsigned short* sv = reinterpret_cast<const unsigned short*>(sg + Lay::V) + v;
-            const unsigned short lamb = (unsigned short)(__float_as_uint(lam) >> 16);     // a power of two: exact
+            const float theta = trans ? 1.f : reinterpret_cast<const float*>(sm + Lay::VM + st * Lay::VMS)[P];
+            const unsigned short lamb = (unsigned short)(__float_as_uint(lam * theta) >> 16);     // a power of two: exact
             const int rows = trans ? 0 : len - (cb + c) * C;      // tokens behind them write nothing
             yl = inverse(lam);
-            // ---- R = V - e^Gamma rk (K S^T), 8 tokens of each half a thread
+            // ---- R = theta (V - e^Gamma rk K S^T), 8 tokens of each half a thread
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 const int t0 = 32 * half + 8 * part;

@@ -774,3 +774,37 @@ def test_wait_gives_up_and_reports(cuda_lib):
         torch.cuda.synchronize()
         assert status.tolist() == [7, 1], limit
     check(make(G=16, H=32, B=5, L=100), "after the probe", segments=1)
+
+
+# ------------------------------------------------------------ tokens that hardly write
+@pytest.mark.parametrize("segments", [1, 3])
+@pytest.mark.parametrize("gate", [-5.0, -8.0, -12.0, -20.0, -60.0])
+@pytest.mark.parametrize("N, P", [(64, 128), (128, 64)])
+def test_small_betas(cuda_lib, N, P, gate, segments):
+    """Every beta near sigmoid(gate), no state to begin with: y and the state are as
+    small as the betas, and as exact as otherwise."""
+    inp = make(N, P, L=330, B=1)
+    inp["b_raw"] = (gate + 0.5 * inp["b_raw"].float()).bfloat16()
+    y, h = run(inp, h0=False, segments=segments)
+    y_ref, h_ref = ref(inp, h0=False)
+    size = np.exp(gate)
+    close(y / size, y_ref / size, 2.6e-3, "y", 1.3e-2)
+    close(h / size, h_ref / size, 1e-5, "state")
+
+
+@pytest.mark.parametrize("segments", [1, 3])
+def test_betas_of_every_size(cuda_lib, segments):
+    """Chunks of large and of small betas in turn, one with none at all, each head after its own pattern."""
+    inp = make(L=450, B=2)
+    gates = torch.tensor([[0., -14., -4., -90., 3., -9., 1., -25.], [-14., 0., -30., 2., -6., -6., 5., 0.],
+                          [-20., -16., -12., -8., -4., 0., 0., 0.], [0., -4., -8., -12., -16., -20., -24., -28.]])
+    inp["b_raw"] = (inp["b_raw"].float() + gates.repeat_interleave(64, 1)[:, :450].T).bfloat16()
+    inp["b_raw"][:, 64:128, 3] = -float("inf")
+    want = {n: t.clone() for n, t in inp.items()}
+    want["b_raw"][:, 64:128, 3] = -1e4
+    for h0 in (False, True):
+        y, h = run(inp, h0=h0, segments=segments)
+        y_ref, h_ref = ref(want, h0=h0)
+        for hd in range(4):
+            close(y[:, :, hd], y_ref[:, :, hd], 2.6e-3, f"y of head {hd}", 1.3e-2)
+            close(h[:, hd], h_ref[:, hd], 1e-5, f"state of head {hd}")
