@@ -42,6 +42,29 @@ __device__ __forceinline__ float softplus_full(float v) {
 __device__ __forceinline__ float delta_log2_decay(float raw, float expA) {
     return -expA * softplus_full(raw) * kLog2e;
 }
+// One token's decay a, and m = a - 1 for a slow one (a >= 1/2).  A float a near 1
+// is up to 2^-25 off, the same way at every token of a like dt, and a state that
+// lasts thousands of tokens would show the sum (7e-5 after 4096 tokens, 1e-4 of a
+// slower one).  m = -2 e^(-x/2) sinh(x/2) cancels nothing; sinh by its
+// series, x/2 <= ln(2)/2: next term below 1e-9.
+struct DeltaDecay {
+    float a, m;
+    __device__ __forceinline__ DeltaDecay(float raw, float expA) {
+        const float x = expA * softplus_full(raw), u = 0.5f * x, v = u * u;
+        a = ex2_approx(-x * kLog2e);
+        m = -x * ex2_approx(-u * kLog2e) * fmaf(v, fmaf(v, fmaf(v, 1.f / 5040.f, 1.f / 120.f), 1.f / 6.f), 1.f);
+    }
+    __device__ __forceinline__ bool slow() const { return a >= 0.5f; }
+    // a as a float whose errors cancel over the tokens t: what 1 + m rounds off,
+    // in steps of 2^-24, decides against t times the golden ratio, mod 1 (evenly
+    // spread over any run of tokens), whether a is one step further.
+    __device__ __forceinline__ float at(uint32_t t) const {
+        const float r = 1.f + m;
+        const float off = (m - (r - 1.f)) * 0x1p24f;                   // exact: within +- 1/2
+        const float s = floorf(off + (float)(t * 2654435769u >> 8) * 0x1p-24f);
+        return slow() ? fmaf(s, 0x1p-24f, r) : a;
+    }
+};
 __device__ __forceinline__ float delta_beta(float b) {
     const float e = exp_neg(fabsf(b));                 // sigmoid without overflow
     const float r = 1.0f / (1.0f + e);
@@ -120,8 +143,9 @@ __global__ void __launch_bounds__(128) delta_step_kernel(DeltaParams p) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) v[r] = Io::load(vp + r * RW);
     const size_t bh = (size_t)b * p.H + h;
-    const float a = ex2_approx(delta_log2_decay(Io::load(static_cast<const T*>(p.dt_raw) + bh) + __ldg(p.dt_bias + h),
-                                                delta_exp_a(__ldg(p.A_log + h))));
+    const DeltaDecay dec(Io::load(static_cast<const T*>(p.dt_raw) + bh) + __ldg(p.dt_bias + h), delta_exp_a(__ldg(p.A_log + h)));
+    const bool slow = dec.slow();                                   // S + m S, else a S: a call knows no token's number
+    const float a = dec.a;
     const float beta = delta_beta(Io::load(static_cast<const T*>(p.b_raw) + bh));
     float kk = 0.f, qq = 0.f, kq = 0.f;
 #pragma unroll
@@ -149,10 +173,15 @@ __global__ void __launch_bounds__(128) delta_step_kernel(DeltaParams p) {
         sq = lane_sum<LPR>(sq);
         const float e = beta * (v[r] - a * rk * sk) * rk;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(st + (size_t)r * RW * N + 4 * LPR * i) =
-                make_float4(fmaf(e, k[4 * i], a * S[r][4 * i]), fmaf(e, k[4 * i + 1], a * S[r][4 * i + 1]),
-                            fmaf(e, k[4 * i + 2], a * S[r][4 * i + 2]), fmaf(e, k[4 * i + 3], a * S[r][4 * i + 3]));
+        for (int i = 0; i < 4; ++i) {
+            float s[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = S[r][4 * i + j];
+                s[j] = fmaf(e, k[4 * i + j], slow ? fmaf(dec.m, x, x) : a * x);
+            }
+            *reinterpret_cast<float4*>(st + (size_t)r * RW * N + 4 * LPR * i) = make_float4(s[0], s[1], s[2], s[3]);
+        }
         if (qd == 0) Io::store(yp + r * RW, rq * fmaf(e, kq, a * sq));
     }
 }
@@ -262,7 +291,7 @@ __global__ void __launch_bounds__(128) delta_recur_kernel(DeltaParams p) {
             kq = lane_sum<8>(kq);
             if (l == 0 && t < nt) {
                 const size_t o = ((size_t)b * p.L + t0 + t) * p.H + h;
-                const float a = ex2_approx(delta_log2_decay(Io::load(static_cast<const T*>(p.dt_raw) + o) + bias, expA));
+                const float a = DeltaDecay(Io::load(static_cast<const T*>(p.dt_raw) + o) + bias, expA).at(t0 + t);
                 const float beta = delta_beta(Io::load(static_cast<const T*>(p.b_raw) + o));
                 sc[t] = make_float4(a, beta, p.norm ? rsqrtf(kk + kDeltaEps) : 1.f,
                                     p.scale * (p.norm ? rsqrtf(qq + kDeltaEps) : 1.f));

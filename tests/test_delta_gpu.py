@@ -808,3 +808,71 @@ def test_betas_of_every_size(cuda_lib, segments):
         for hd in range(4):
             close(y[:, :, hd], y_ref[:, :, hd], 2.6e-3, f"y of head {hd}", 1.3e-2)
             close(h[:, hd], h_ref[:, hd], 1e-5, f"state of head {hd}")
+
+
+# ------------------------------------------------------------ long memories token by token
+SLOW = [(-3.0, None), (-6.0, -4.0), (-8.0, -4.0), (-8.0, None), (-10.0, -4.0), (-14.0, -9.0)]
+
+
+def slow(db, b, L, io="f32", const=True):
+    """Tokens whose decays are all alike and keep some e^-db of them, and which replace little."""
+    inp = make(64, 128, G=1, H=2, io=io, L=L, B=1)
+    inp["dt_bias"][:] = torch.tensor([db, db - 1])
+    inp["A_log"][:] = 0.0
+    if const:
+        inp["dt_raw"][:] = 0.3
+    if b is not None:
+        inp["b_raw"][:] = b
+    return inp
+
+
+def slow_tol(db, n):
+    """An element of the state is rounded three times a token, to either side: sqrt(3 n)
+    2^-25 / sqrt(3), 2e-6 of n = 4096, asserted at 1e-5.  But where a token takes off few
+    steps of an element, S - (1 - a) S with (1 - a) < 2^-17, or 2^7 steps of 2^-24 at most,
+    the difference is rounded the same way at token after token until the element has
+    changed by a good part of itself, which it does not: at most half a step, 2^-24 of the
+    element, n times.  That is the float32 state's own limit, whatever a is known to."""
+    return 1e-5 if np.exp(db - 1) >= 2 ** -17 else n * 2 ** -24
+
+
+@pytest.mark.parametrize("const", [True, False])
+@pytest.mark.parametrize("db, b", SLOW)
+def test_long_memory_token_by_token(cuda_lib, db, b, const):
+    inp, tol = slow(db, b, 4096, const=const), slow_tol(db, 4096)
+    y, h = run(inp)
+    y_ref, h_ref = ref(inp)
+    close(y, y_ref, tol, "y")
+    close(h, h_ref, tol, "state")
+
+
+@pytest.mark.parametrize("db, b", SLOW)
+def test_long_memory_of_steps(cuda_lib, db, b):
+    from selective_state_space_52_b200 import axon_ssm
+    inp = slow(db, b, 3000)
+    d, params = dev(inp)
+    state = d["h0"].clone()
+    seq = [d[n].unbind(1) for n in SEQ]
+    ys = [axon_ssm.delta_step(*t, params, state) for t in zip(*seq)]
+    y_ref, h_ref = ref(inp)
+    close(torch.stack(ys, 1).cpu().numpy(), y_ref, slow_tol(db, 3000), "y")
+    close(state.cpu().numpy(), h_ref, slow_tol(db, 3000), "state")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_every_rate_of_decay(cuda_lib, io):
+    """Decays of one token from 1 to 0 past the middle, where the state's form of it changes; no writes beside them."""
+    L = 40
+    inp = make(G=1, H=4, io=io, L=L, B=1)
+    inp["A_log"][:] = 0.0
+    inp["dt_bias"][:] = torch.tensor([-20.0, -0.001, 0.001, 4.0])
+    inp["dt_raw"] = torch.linspace(-1, 1, L)[None, :, None].expand(1, L, 4).to(inp["dt_raw"].dtype).contiguous()
+    inp["v"][:] = 0
+    inp["b_raw"][:] = -100.0
+    want, _ = ref(inp)
+    y, h = run(inp)
+    for t in range(12):
+        close(y[:, t], want[:, t], tols(io)[0], f"y of token {t}", 4e-4 if io == "f32" else 1.3e-2)
+        for hd in range(4):
+            r = want[0, t, hd]
+            assert np.linalg.norm(y[0, t, hd] - r) <= (3e-5 if io == "f32" else 2.6e-3) * np.linalg.norm(r) + 1e-36, (t, hd)
