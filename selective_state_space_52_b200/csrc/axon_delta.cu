@@ -118,10 +118,12 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // Segments of whole chunks.  One walk runs on an SM at a time, so a pass takes
 // ceil(walks / SMs) rounds of one segment's chunks; a chunk of the pass
-// without outputs takes as long as one with them (2.9 us: the same chain of
+// without outputs takes nearly as long as one with them (2.8 and 3.3 us: the same chain of
 // products and conversions), a round's start about 2.5 chunks, a fold half of
-// one, and the second launch about two.  B1 L4096 H32 measured 247, 236, 186, 205, 230 us at 1 to 5
-// segments.  `requested` > 0 asks for that many.
+// one, and the second launch about two.  B1 L4096 H32 measured 261, 248, 193,
+// 214, 243 us at 1 to 5 segments; N = P = 64, B2 L2047 H16: 119, 111, 91, 98,
+// 102 (three are taken both times).  L counts, not where rows end: lengths lie
+// on the device.  `requested` > 0 asks for that many.
 struct DeltaPlan {
     int segs, cps;
 };

@@ -136,11 +136,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 // ---- prep: grid = (nC, G, B), 128 threads.  What bounds it is latency and the
-// instruction caches (six blocks an SM in different phases), so the loops are
+// instruction caches (five blocks an SM in different phases, six at N = 64), so the loops are
 // kept short: forward substitution down whole columns, unrolled over
 // registers, took 15 to 24 thousand cycles a head where this takes three.
-// 4096 tokens of 32 heads on 16 key heads, N = 128: 47 us, 43% of issue slots,
-// 62 MB from and to HBM.
+// 4096 tokens of 32 heads on 16 key heads, N = 128: 49 us, 41% of issue slots,
+// 65 MB from and to HBM.
 template <int N>
 struct DeltaPrepSmem {
     static constexpr int LDA = 68;                       // floats a row of A: 16-byte rows without bank conflicts
@@ -526,9 +526,10 @@ __global__ void __launch_bounds__(128, 6) delta_prep_kernel(DeltaChunkParams p) 
 // the state row and of the tokens.  (One warp a quadrant, two blocks an SM,
 // took 12 thousand cycles a chunk: with one warp a scheduler nothing hides the
 // latencies of the conversions.)  Warp 16 copies tiles in and issues products,
-// warp 17 finds the columns' largest |v| a chunk ahead.  A chunk takes 2.9 us
-// (N = P = 128): 4096 tokens of 32 heads in three segments, 69 us without and
-// 80 us with outputs, tensor pipe 28% and issue slots 53% busy.
+// warp 17 finds theta and the columns' largest |v| a chunk ahead.  A chunk takes
+// 2.8 us without outputs and 3.3 with (N = P = 128): 4096 tokens of 32 heads in three segments, 70 us
+// without and 88 us with outputs, tensor pipe 32% and issue slots 52% busy.
+// The second parts of Y's operands and theta are 8 of those 88.
 constexpr int kDlThreads = 576;
 constexpr int kDlStages = 3;
 
