@@ -310,6 +310,40 @@ def axon_delta_workspace_bytes(B, L, H, G, P=128, N=128, io=AXON_BF16, segments=
     return int(_lib.axon_delta_workspace_bytes(B, L, H, G, P, N, io, segments))
 
 
+def _v(t):
+    """Device pointer of a tensor that may be a view with a row stride."""
+    return t if t is None or isinstance(t, int) else t.data_ptr()
+
+
+def axon_delta_scan_fwd(B, L, H, G, P, N, io, q, ldq, k, ldk, v, ldv, dt_raw, b_raw, dt_bias, A_log, lengths, h0,
+                        scale, qk_norm, y, h_out, segments, workspace, workspace_bytes, stream=None, *,
+                        raise_on_error=True) -> int:
+    rc = _lib.axon_delta_scan_fwd(B, L, H, G, P, N, io, _v(q), ldq, _v(k), ldk, _v(v), ldv, _p(dt_raw), _p(b_raw),
+                                  _p(dt_bias), _p(A_log), _p(lengths), _p(h0), scale, qk_norm, _p(y), _p(h_out),
+                                  segments, _p(workspace), int(workspace_bytes), _stream(stream))
+    if raise_on_error:
+        _check(rc, "axon_delta_scan_fwd")
+    return rc
+
+
+def axon_delta_step(B, H, G, P, N, io, q, ldq, k, ldk, v, ldv, dt_raw, b_raw, dt_bias, A_log, scale, qk_norm, state,
+                    y, stream=None, *, raise_on_error=True) -> int:
+    rc = _lib.axon_delta_step(B, H, G, P, N, io, _v(q), ldq, _v(k), ldk, _v(v), ldv, _p(dt_raw), _p(b_raw),
+                              _p(dt_bias), _p(A_log), scale, qk_norm, _p(state), _p(y), _stream(stream))
+    if raise_on_error:
+        _check(rc, "axon_delta_step")
+    return rc
+
+
+def axon_gated_norm_fwd(rows, C, D, io, kind, gate, act, x, ldx, z, ldz, weight, bias, per_channel, eps, y, ldy,
+                        stream=None, *, raise_on_error=True) -> int:
+    rc = _lib.axon_gated_norm_fwd(rows, C, D, io, kind, gate, act, _v(x), ldx, _v(z), ldz, _p(weight), _p(bias),
+                                  per_channel, eps, _v(y), ldy, _stream(stream))
+    if raise_on_error:
+        _check(rc, "axon_gated_norm_fwd")
+    return rc
+
+
 def axon_delta_wait_probe(status, limit, stream=None, *, raise_on_error=True) -> int:
     rc = _lib.axon_delta_wait_probe(_p(status), int(limit), _stream(stream))
     if raise_on_error:
@@ -854,6 +888,6 @@ def gated_norm(x, weight=None, z=None, *, bias=None, group=None, kind="rms", gat
         ldx, ldy, ldz = (0 if t is None else _row_stride("gated_norm", name, t, rows, C)
                          for name, t in (("x", x), ("out", y), ("z", z)))
     _check(_lib.axon_gated_norm_fwd(rows, C, D, _dtype_code(x.dtype), NORM_KINDS[kind], 0 if z is None else NORM_GATES[gate],
-                                    act, x.data_ptr(), ldx, None if z is None else z.data_ptr(), ldz, _p(weight), _p(bias),
+                                    act, x.data_ptr(), ldx, _v(z), ldz, _p(weight), _p(bias),
                                     n == C and n != D, eps, y.data_ptr(), ldy, _stream_on(stream, i)), "axon_gated_norm_fwd")
     return y

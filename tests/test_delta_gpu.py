@@ -876,3 +876,33 @@ def test_every_rate_of_decay(cuda_lib, io):
         for hd in range(4):
             r = want[0, t, hd]
             assert np.linalg.norm(y[0, t, hd] - r) <= (3e-5 if io == "f32" else 2.6e-3) * np.linalg.norm(r) + 1e-36, (t, hd)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_bindings_of_the_c_entries(cuda_lib, io):
+    """The binding's functions of the C names, called with every argument, as the convenience calls give them."""
+    from selective_state_space_52_b200 import axon_ssm
+    inp = make(64, 128, 2, 4, io, L=130, B=2)
+    d, params = dev(inp)
+    code = axon_ssm.AXON_F32 if io == "f32" else axon_ssm.AXON_BF16
+    gates = (d["dt_raw"], d["b_raw"], d["dt_bias"], d["A_log"])
+    qkv = (d["q"], 128, d["k"], 128, d["v"], 512)
+    lengths = torch.tensor([130, 77], dtype=torch.int32, device="cuda")
+    n = axon_ssm.axon_delta_workspace_bytes(2, 130, 4, 2, 128, 64, code, 2 if io == "bf16" else 0)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    y, h = torch.zeros_like(d["v"]), torch.empty_like(d["h0"])
+    seg = 2 if io == "bf16" else 0
+    assert axon_ssm.axon_delta_scan_fwd(2, 130, 4, 2, 128, 64, code, *qkv, *gates, lengths, d["h0"], 0.3, 1, y, h, seg, ws, n) == 0
+    want = axon_ssm.delta_scan(*(d[m] for m in SEQ), params, d["h0"], lengths=lengths, scale=0.3, segments=seg,
+                               out=(torch.zeros_like(y), torch.empty_like(h)))
+    assert torch.equal(y, want[0]) and torch.equal(h, want[1])
+    one = [d[m][:, 5].contiguous() for m in SEQ]
+    y1, s1, s2 = torch.empty_like(one[2]), d["h0"].clone(), d["h0"].clone()
+    axon_ssm.axon_delta_step(2, 4, 2, 128, 64, code, one[0], 128, one[1], 128, one[2], 512, one[3], one[4], d["dt_bias"],
+                             d["A_log"], 0.3, 0, s1, y1)
+    y2 = axon_ssm.delta_step(*one, params, s2, scale=0.3, qk_norm=False)
+    assert torch.equal(y1, y2) and torch.equal(s1, s2)
+    x, z, w, b = d["v"].flatten(2), d["v"].flatten(2).flip(1).contiguous(), torch.rand(512, device="cuda"), torch.rand(512, device="cuda")
+    o = torch.empty_like(x)
+    axon_ssm.axon_gated_norm_fwd(260, 512, 128, code, 1, 2, 1, x, 512, z, 512, w, b, 1, 1e-5, o, 512)
+    assert torch.equal(o, axon_ssm.gated_norm(x, w, z, bias=b, group=128, kind="group", gate="before", eps=1e-5))
