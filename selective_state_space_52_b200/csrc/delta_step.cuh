@@ -56,12 +56,13 @@ struct DeltaDecay {
     }
     __device__ __forceinline__ bool slow() const { return a >= 0.5f; }
     // a as a float whose errors cancel over the tokens t: what 1 + m rounds off,
-    // in steps of 2^-24, decides against t times the golden ratio, mod 1 (evenly
-    // spread over any run of tokens), whether a is one step further.
+    // in steps of 2^-24, decides against t times the golden ratio plus a half, mod
+    // 1 (evenly spread over any run of tokens; a lone one is rounded to nearest),
+    // whether a is one step further.
     __device__ __forceinline__ float at(uint32_t t) const {
         const float r = 1.f + m;
         const float off = (m - (r - 1.f)) * 0x1p24f;                   // exact: within +- 1/2
-        const float s = floorf(off + (float)(t * 2654435769u >> 8) * 0x1p-24f);
+        const float s = floorf(off + (float)(t * 2654435769u + 0x80000000u >> 8) * 0x1p-24f);
         return slow() ? fmaf(s, 0x1p-24f, r) : a;
     }
 };
