@@ -430,13 +430,13 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * sqrt(2 / beta) let the state grow without bound, and bf16 prefill in chunks,
  * whose products take fp16 parts, is made for keys of length near 1: with
  * longer ones than about 4 an operand can leave fp16's range, which shows as
- * infinity or NaN and in the error flag; with all keys at length l < 1 the state's relative error
- * is some 1e-6 / l.  Queries may have any length.  In chunks the state before
- * 64 tokens and what they write, a value column at a time, keep 21 bits of
- * the larger of the two: writes smaller by more than that than a state which
- * the same chunk forgets are lost.  Token by token neither limit holds.
- * |k|^2 and |q|^2 are float32: with the norm, rows longer than 1.8e19 count
- * as zeros.)
+ * infinity or NaN and in the error flag; with all keys at length l < 1 the
+ * state's relative error is some 1e-6 / l.  Queries may have any length.  In
+ * chunks the state before 64 tokens and what they write, a value column at a
+ * time, keep 21 bits of the larger of the two: writes smaller by more than
+ * that than a state which the same chunk forgets are lost.  Token by token
+ * neither limit holds. |k|^2 and |q|^2 are float32: with the norm, rows longer
+ * than 1.8e19 count as zeros.)
  *
  * axon_delta_scan_fwd, prefill.  Layouts: q, k (B,L,G,N) and v (B,L,H,P) io,
  * consecutive tokens ldq, ldk, ldv elements apart (ldq, ldk >= G*N, ldv >=
@@ -469,9 +469,8 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * a kernel for its copies or products gave up (the outputs are then undefined),
  * bit 1 if, with qk_norm == 0, y or the end state is not finite: an operand
  * left fp16's range, or an input was not finite.  Read it after the call
- * completes.  Every call writes what it reads in the
- * workspace, so calls that may run at the same time (streams, captured graphs)
- * need one each.  Pointers 16-byte aligned (dt_raw, b_raw, dt_bias, A_log and
+ * completes.  Every call writes what it reads in the workspace, so calls that
+ * may run at the same time (streams, captured graphs) need one each.  Pointers 16-byte aligned (dt_raw, b_raw, dt_bias, A_log and
  * lengths: by their own element) and ldq, ldk, ldv multiples of 8 (bf16) or 4
  * (f32), else AXON_ERR_ALIGNMENT; y, h_out and the
  * workspace overlap no input (but h_out may be h0) nor each other
@@ -480,9 +479,10 @@ AXON_API axon_status axon_ssd_scan_fwd(
  * zeros) to h_out.  A NaN or infinity in a token of a row shows in its head's
  * outputs from then on, and in chunks it may from the chunk's start.
  * The state and all sums are float32.  In chunks the operands of the tensor
- * core products are rounded further: every one but q and k (which are exact)
- * enters as two fp16 parts, 21 significant bits of it; y is rounded once, to
- * its io type.  Other conventions as above.
+ * core products are rounded further: each enters as two fp16 parts, 21
+ * significant bits of it, but for q and k, which are exact down to 2^-25 of a
+ * row's largest element; y is rounded once, to its io type.  Other
+ * conventions as above.
  */
 AXON_API size_t axon_delta_workspace_bytes(int B, int L, int H, int G, int P, int N, axon_dtype io, int segments);
 
@@ -529,7 +529,9 @@ AXON_API axon_status axon_delta_step(
  * C (AXON_ERR_INVALID_ARG) and is a multiple of 8 (bf16) or 4 (f32), as are
  * ldx, ldz, ldy (AXON_ERR_ALIGNMENT); D <= 8192 and rows * C / D <= 2^31 - 4096, else
  * AXON_ERR_UNSUPPORTED.  eps >= 0; a group of zeros with eps == 0 gives NaN.
- * rows == 0 is a no-op.  Float32 inside, rounded once.
+ * rows == 0 is a no-op.  Float32 inside, rounded once; squares are float32
+ * too, so values above 1.8e19 overflow the statistics (their group gives
+ * zeros or NaN) and values below 1e-19 add nothing to them.
  */
 typedef enum {
     AXON_NORM_RMS = 0,
